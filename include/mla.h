@@ -325,6 +325,58 @@ mla_status mla_prefill_attn(const void* ckr, const void* q_nope, const void* q_r
                             float scale, void* out, void* workspace, size_t workspace_bytes, mla_dims d,
                             void* stream);
 
+/* ---------------------------------------------------------------- the layer around the attention
+ * What stands directly before and after this path in its layer: the norm of the residual
+ * stream, the projections that make the queries, the optional output gate and Wo with the
+ * residual's addition (kimi-k3 docs "GatedMLA", "Projection geometry and stored weights"
+ * and "Output projection and optional gate"). All sums and statistics are fp32; each
+ * output element is rounded once, where it is stored. Any sizes: no dims, no workspace.
+ *
+ * Residual addition and RMS norm of rows x [T][M]:
+ *   s = x + residual (s = x without one),  residual_out = s,
+ *   out = s * gain / sqrt(mean(s^2) + eps)      (of the fp32 s, not of the stored one)
+ *   x, residual, residual_out, out [T][M], gain [M]: dtype (MLA_BF16 or MLA_F32)
+ * residual and residual_out are both given or both NULL. residual_out may be residual or
+ * x, out may be x or residual (the same buffer, for at most one of the two); outputs
+ * overlap nothing otherwise (MLA_ERR_INVALID). A row of zeros with eps = 0 gives NaN, as
+ * the formula does; a row with a NaN or an infinity affects no other row.              */
+mla_status mla_add_rmsnorm(const void* x, const void* residual, const void* gain, void* residual_out, void* out,
+                           int32_t T, int32_t M, float eps, int32_t dtype, void* stream);
+
+/* The same with an 8-bit output: codes [T][M] and scales [T], rows in the format of the
+ * 8-bit cache above (E4M3 codes of the fp32 result, one power-of-two scale byte per row;
+ * rounded once, from fp32). `out` (dtype) may be NULL, or is written beside the codes, for
+ * a layer whose cache write takes bf16 rows and whose projections take 8-bit ones. A NaN
+ * gets the NaN code 0x7F or 0xFF and does not count towards its row's scale.             */
+mla_status mla_add_rmsnorm_fp8(const void* x, const void* residual, const void* gain, void* residual_out, void* out,
+                               void* codes, void* scales, int32_t T, int32_t M, float eps, int32_t dtype,
+                               void* stream);
+
+/* Quantises n rows of any width (dtype) into that format: codes [n][width], scales [n];
+ * for the weights and inputs of mla_linear_fp8 (mla_quantize_rows_fp8 is the cache's). */
+mla_status mla_quantize_fp8(const void* rows, void* codes, void* scales, int32_t n, int32_t width, int32_t dtype,
+                            void* stream);
+
+/* Activation of the projections: v, 1 / (1 + e^-v), v / (1 + e^-v), or v Phi(v) with the
+ * normal distribution function Phi (the erf form). */
+typedef enum { MLA_ACT_NONE = 0, MLA_ACT_SIGMOID = 1, MLA_ACT_SILU = 2, MLA_ACT_GELU = 3 } mla_act;
+
+/* out[t][n] = residual[t][n] + mul[t][n] * act(sum_k x[t][k] W[n][k] + bias[n])
+ *   x [T][K], W [N][K] (out x in, as W_DKV), bias [N], mul [T][N], residual [T][N],
+ *   out [T][N]: bf16. bias, mul and residual may each be NULL (0, 1 and 0).
+ * mul serves the output gate (sigmoid(x Wg^T) * attention) and a gated feed-forward's
+ * silu(x Wg^T) * (x Wu^T). out may be mul's or residual's buffer; it overlaps nothing
+ * otherwise (MLA_ERR_INVALID).                                                          */
+mla_status mla_linear(const void* x, const void* W, const void* bias, const void* mul, const void* residual, void* out,
+                      int32_t T, int32_t N, int32_t K, int32_t act, void* stream);
+
+/* The same with 8-bit x and W: x_codes [T][K], W_codes [N][K] (E4M3), x_scales [T],
+ * W_scales [N] (scale bytes); the products of the codes are summed in fp32 and both scales
+ * multiply the sum. bias, mul, residual and out are bf16.                               */
+mla_status mla_linear_fp8(const void* x_codes, const void* x_scales, const void* W_codes, const void* W_scales,
+                          const void* bias, const void* mul, const void* residual, void* out, int32_t T, int32_t N,
+                          int32_t K, int32_t act, void* stream);
+
 /* ---------------------------------------------------------------- allocation-free decode
  * The pages describe no counterpart of this call; it exists for callers that cannot
  * allocate device memory: code inside another framework's fixed memory pool, or a

@@ -19,6 +19,7 @@ LIB_PATH = os.environ.get("MLA_LIBRARY") or os.path.join(_PKG, "_lib", "libmla.s
 MLA_OK, MLA_ERR_INVALID, MLA_ERR_UNSUPPORTED, MLA_ERR_WORKSPACE, MLA_ERR_CUDA, MLA_ERR_TIMEOUT = 0, -1, -2, -3, -4, -5
 MLA_BF16, MLA_F32 = 0, 1
 MLA_POLICY_AUTO, MLA_POLICY_SIMT, MLA_POLICY_TCGEN05 = 0, 1, 2
+MLA_ACT_NONE, MLA_ACT_SIGMOID, MLA_ACT_SILU, MLA_ACT_GELU = 0, 1, 2, 3
 
 STATUS_NAMES = {0: "MLA_OK", -1: "MLA_ERR_INVALID", -2: "MLA_ERR_UNSUPPORTED", -3: "MLA_ERR_WORKSPACE",
                 -4: "MLA_ERR_CUDA", -5: "MLA_ERR_TIMEOUT"}
@@ -28,7 +29,8 @@ EXPORTS = ("mla_abi_version", "mla_last_error", "mla_set_policy", "mla_set_wait_
            "mla_check_status", "mla_cache_append", "mla_cache_write", "mla_cache_write_workspace_size", "mla_absorb_q", "mla_plan_capacity", "mla_plan_splits",
            "mla_workspace_size", "mla_decode_attn", "mla_combine", "mla_out_proj", "mla_decode_attn_noalloc",
            "mla_debug_drop_page_load", "mla_quantize_rows_fp8", "mla_cache_append_fp8", "mla_workspace_size_fp8",
-           "mla_decode_attn_fp8", "mla_prefill_workspace_size", "mla_prefill_attn")
+           "mla_decode_attn_fp8", "mla_prefill_workspace_size", "mla_prefill_attn", "mla_add_rmsnorm", "mla_add_rmsnorm_fp8",
+           "mla_quantize_fp8", "mla_linear", "mla_linear_fp8")
 
 
 class MlaError(RuntimeError):
@@ -84,6 +86,11 @@ def _load():
         "mla_decode_attn_fp8": (I32, [P, P, P, P, P, P, I32, I32, I32, I32, F, P, INFO, P, P, P, SZ, D, P]),
         "mla_prefill_workspace_size": (SZ, [I32, D]),
         "mla_prefill_attn": (I32, [P, P, P, P, P, P, P, I32, F, P, P, SZ, D, P]),
+        "mla_add_rmsnorm": (I32, [P, P, P, P, P, I32, I32, F, I32, P]),
+        "mla_add_rmsnorm_fp8": (I32, [P, P, P, P, P, P, P, I32, I32, F, I32, P]),
+        "mla_quantize_fp8": (I32, [P, P, P, I32, I32, I32, P]),
+        "mla_linear": (I32, [P, P, P, P, P, P, I32, I32, I32, I32, P]),
+        "mla_linear_fp8": (I32, [P, P, P, P, P, P, P, P, I32, I32, I32, I32, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -252,3 +259,40 @@ def mla_prefill_attn(ckr, q_nope, q_rope, W_UK, W_UV, cu_seqlens, cu_seqlens_hos
     _check(_lib.mla_prefill_attn(_ptr(ckr), _ptr(q_nope), _ptr(q_rope), _ptr(W_UK), _ptr(W_UV), _ptr(cu_seqlens),
                                  host.ctypes.data, B, scale, _ptr(out), _ptr(workspace), workspace_bytes, dims,
                                  _stream(stream)), "mla_prefill_attn")
+
+
+def _dense(x):
+    """data_ptr of a contiguous tensor (None -> NULL, integers are raw addresses); the
+    calls take row-major buffers only, so a strided view is refused, not misread."""
+    if x is None or isinstance(x, int):
+        return x
+    if not x.is_contiguous():
+        raise MlaError(MLA_ERR_INVALID, "argument", "tensor is not contiguous")
+    return x.data_ptr()
+
+
+def mla_add_rmsnorm(x, residual, gain, residual_out, out, T, M, eps, dtype, stream=None):
+    _check(_lib.mla_add_rmsnorm(_dense(x), _dense(residual), _dense(gain), _dense(residual_out), _dense(out), T, M,
+                                eps, dtype, _stream(stream)), "mla_add_rmsnorm")
+
+
+def mla_add_rmsnorm_fp8(x, residual, gain, residual_out, out, codes, scales, T, M, eps, dtype, stream=None):
+    _check(_lib.mla_add_rmsnorm_fp8(_dense(x), _dense(residual), _dense(gain), _dense(residual_out), _dense(out),
+                                    _dense(codes), _dense(scales), T, M, eps, dtype, _stream(stream)),
+           "mla_add_rmsnorm_fp8")
+
+
+def mla_quantize_fp8(rows, codes, scales, n, width, dtype, stream=None):
+    _check(_lib.mla_quantize_fp8(_dense(rows), _dense(codes), _dense(scales), n, width, dtype, _stream(stream)),
+           "mla_quantize_fp8")
+
+
+def mla_linear(x, W, bias, mul, residual, out, T, N, K, act, stream=None):
+    _check(_lib.mla_linear(_dense(x), _dense(W), _dense(bias), _dense(mul), _dense(residual), _dense(out), T, N, K,
+                           act, _stream(stream)), "mla_linear")
+
+
+def mla_linear_fp8(x_codes, x_scales, W_codes, W_scales, bias, mul, residual, out, T, N, K, act, stream=None):
+    _check(_lib.mla_linear_fp8(_dense(x_codes), _dense(x_scales), _dense(W_codes), _dense(W_scales), _dense(bias),
+                               _dense(mul), _dense(residual), _dense(out), T, N, K, act, _stream(stream)),
+           "mla_linear_fp8")

@@ -1,0 +1,112 @@
+// linear.cuh -- the layer's projections: out = residual + mul * act(x W^T + bias), with
+// W stored out x in. The epilogue every kernel shares, and the CUDA-core kernel for
+// geometries the tensor-core kernels (linear_tc.cuh) do not take.
+//
+// Sums are fp32; bias, activation, mul and residual are applied to the fp32 sum and the
+// result is rounded once, to bf16. 8-bit operands are E4M3 codes with one power-of-two
+// scale per row of x and of W (see fp8_kernels.cuh): the codes' products are summed and the
+// two scales multiply the sum, exactly.
+#pragma once
+
+#include "common.cuh"
+#include "fp8_kernels.cuh"
+
+namespace mla {
+namespace lin {
+
+enum : int { kActNone = 0, kActSigmoid = 1, kActSilu = 2, kActGelu = 3 };
+
+struct Params {
+  const __nv_bfloat16* bias;   // [N] or null
+  const __nv_bfloat16* mul;    // [T][N] or null
+  const __nv_bfloat16* res;    // [T][N] or null
+  __nv_bfloat16* out;          // [T][N]
+  const uint8_t* xs;           // [T] scale bytes (8-bit operands)
+  const uint8_t* ws;           // [N]
+  int32_t T, N, K, act;
+  uint64_t timeout_ns;
+};
+
+// 2^(byte - 127); the bytes the quantisers write are 1 .. 134.
+__device__ __forceinline__ float scale_of(uint8_t b) { return __uint_as_float((uint32_t)b << 23); }
+
+__device__ __forceinline__ float activate(float v, int act) {
+  switch (act) {
+    case kActSigmoid: return 1.f / (1.f + __expf(-v));
+    case kActSilu: return v / (1.f + __expf(-v));
+    case kActGelu: return 0.5f * v * erfcf(-0.70710678118654752f * v);
+    default: return v;
+  }
+}
+
+// One output element from its fp32 sum (8-bit operands: already times both scales).
+__device__ __forceinline__ void finish(const Params& p, float v, int64_t t, int32_t n, float bias) {
+  const int64_t at = t * p.N + n;
+  v = activate(v + bias, p.act);
+  if (p.mul) v *= __bfloat162float(p.mul[at]);
+  if (p.res) v += __bfloat162float(p.res[at]);
+  p.out[at] = __float2bfloat16_rn(v);
+}
+
+// ------------------------------------------------------------------ CUDA cores
+// A block of 256 threads computes 64 tokens x 64 features, 16 K elements at a time through
+// shared memory, 4 x 4 sums per thread. Any size and alignment. Blocks are numbered along
+// the token tiles first, so that neighbours share a weight tile.
+constexpr int kTile = 64, kStep = 16;
+
+template <bool F8>
+__global__ void __launch_bounds__(256) linear_simt_kernel(const void* __restrict__ x, const void* __restrict__ W,
+                                                          const Params p) {
+  __shared__ float sx[kStep][kTile + 4], sw[kStep][kTile + 4];
+  const int tiles_t = (p.T + kTile - 1) / kTile;
+  const int t0 = (blockIdx.x % tiles_t) * kTile, n0 = (blockIdx.x / tiles_t) * kTile;
+  const int tid = threadIdx.x;
+  const int ty = tid / 16, tx = tid % 16;     // tokens 4 ty .., features tx, tx + 16, ..
+  auto fetch = [&](const void* base, int64_t row, int64_t rows, int k) -> float {
+    if (row >= rows || k >= p.K) return 0.f;
+    const int64_t at = row * p.K + k;
+    if constexpr (F8) return f8::from_e4m3x2(static_cast<const uint8_t*>(base)[at]).x;
+    else return __bfloat162float(static_cast<const __nv_bfloat16*>(base)[at]);
+  };
+  float acc[4][4] = {};
+  for (int k0 = 0; k0 < p.K; k0 += kStep) {
+#pragma unroll
+    for (int i = 0; i < kTile * kStep / 256; ++i) {
+      const int e = tid + 256 * i, r = e / kStep, k = e % kStep;
+      sx[k][r] = fetch(x, t0 + r, p.T, k0 + k);
+      sw[k][r] = fetch(W, n0 + r, p.N, k0 + k);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kStep; ++k) {
+      float a[4], b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = sx[k][4 * ty + i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[j] = sw[k][tx + 16 * j];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] += a[i] * b[j];
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int n = n0 + tx + 16 * j;
+    if (n >= p.N) continue;
+    const float bias = p.bias ? __bfloat162float(p.bias[n]) : 0.f;
+    const float ws = F8 ? scale_of(p.ws[n]) : 1.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int t = t0 + 4 * ty + i;
+      if (t >= p.T) continue;
+      float v = acc[i][j];
+      if (F8) v = v * ws * scale_of(p.xs[t]);
+      finish(p, v, t, n, bias);
+    }
+  }
+}
+
+}  // namespace lin
+}  // namespace mla

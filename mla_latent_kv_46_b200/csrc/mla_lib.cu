@@ -11,6 +11,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -25,6 +26,8 @@
 #include "cache_write.cuh"
 #include "fp8_kernels.cuh"
 #include "prefill.cuh"
+#include "add_rmsnorm.cuh"
+#include "linear.cuh"
 
 namespace {
 
@@ -1232,6 +1235,199 @@ mla_status mla_decode_attn_noalloc(const void* q_lat, const void* q_rope, const 
                                      ws ? kNoAllocScratchBytes : 0, d, stream))
     return s;
   return mla_combine(plan_dev, info, ws, ws ? kNoAllocScratchBytes : 0, o_lat, lse, d, stream);
+}
+
+// ------------------------------------------------------------------------------- residual add + RMS norm
+}  // extern "C"
+
+namespace {
+
+// The widest power-of-two number of elements, at most `most`, that divides the row and
+// keeps every given pointer's rows aligned to its size.
+int vec_elems(int32_t M, int esize, std::initializer_list<const void*> rows, const void* codes) {
+  for (int ve = 16 / esize; ve > 1; ve /= 2) {
+    bool fits = M % ve == 0 && reinterpret_cast<uintptr_t>(codes) % ve == 0;
+    for (const void* q : rows) fits = fits && reinterpret_cast<uintptr_t>(q) % (size_t)(ve * esize) == 0;
+    if (fits) return ve;
+  }
+  return 1;
+}
+
+template <typename T, int VE, int EPT>
+mla_status launch_rms_ept(const mla::rms::Params& p, cudaStream_t st) {
+  constexpr int kItems = EPT / VE;
+  const int chunks = p.M / VE;
+  if (chunks <= 32 * kItems) {
+    const unsigned blocks = (unsigned)(((int64_t)p.T + mla::rms::kWarpRows - 1) / mla::rms::kWarpRows);
+    mla::rms::add_rmsnorm_kernel<T, VE, kItems, true><<<blocks, 32 * mla::rms::kWarpRows, 0, st>>>(p);
+  } else {
+    const int threads = ((chunks + kItems - 1) / kItems + 31) / 32 * 32;
+    mla::rms::add_rmsnorm_kernel<T, VE, kItems, false><<<(unsigned)p.T, threads, 0, st>>>(p);
+  }
+  return launch_check("add_rmsnorm");
+}
+
+template <typename T, int VE>
+mla_status launch_rms_ve(const mla::rms::Params& p, cudaStream_t st) {
+  if (p.M <= 8 * 1024) return launch_rms_ept<T, VE, 8>(p, st);
+  if (p.M <= 16 * mla::rms::max_threads(16)) return launch_rms_ept<T, VE, 16>(p, st);
+  mla::rms::add_rmsnorm_wide_kernel<T><<<(unsigned)p.T, 1024, 0, st>>>(p);
+  return launch_check("add_rmsnorm");
+}
+
+template <typename T>
+mla_status launch_rms(const mla::rms::Params& p, cudaStream_t st) {
+  const int ve = vec_elems(p.M, sizeof(T), {p.x, p.r, p.gain, p.r_out, p.y}, p.codes);
+  if constexpr (sizeof(T) == 2)
+    if (ve == 8) return launch_rms_ve<T, 8>(p, st);
+  if (ve == 4) return launch_rms_ve<T, 4>(p, st);
+  if (ve == 2) return launch_rms_ve<T, 2>(p, st);
+  return launch_rms_ve<T, 1>(p, st);
+}
+
+struct Span {
+  const void* p;
+  size_t bytes;
+};
+bool overlap(const Span& a, const Span& b) {
+  if (!a.p || !b.p) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x < y + b.bytes && y < x + a.bytes;
+}
+// An output may be an input's own buffer where every element is read by the thread that
+// writes it; it may not overlap an input in any other way.
+bool overlap_shifted(const Span& a, const Span& b) { return a.p != b.p && overlap(a, b); }
+
+mla_status add_rmsnorm(const char* what, const void* x, const void* residual, const void* gain, void* residual_out,
+                       void* out, void* codes, void* scales, int32_t T, int32_t M, float eps, int32_t dtype,
+                       bool with_codes, void* stream) {
+  if (T < 0 || M <= 0) return fail(MLA_ERR_INVALID, "%s: bad sizes T=%d M=%d", what, T, M);
+  if (dtype != MLA_BF16 && dtype != MLA_F32)
+    return fail(MLA_ERR_INVALID, "%s: dtype must be MLA_BF16 or MLA_F32, got %d", what, dtype);
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(MLA_ERR_INVALID, "%s: eps must be finite and >= 0", what);
+  if (T == 0) return ok();
+  if (!x || !gain || (with_codes ? !codes || !scales : !out)) return fail(MLA_ERR_INVALID, "%s: null pointer", what);
+  if (!residual != !residual_out)
+    return fail(MLA_ERR_INVALID, "%s: residual and residual_out go together (both or neither)", what);
+  const size_t es = dtype == MLA_BF16 ? 2 : 4, n = (size_t)T * M;
+  for (const void* q : {x, residual, gain, (const void*)residual_out, (const void*)out})
+    if (reinterpret_cast<uintptr_t>(q) % es != 0)
+      return fail(MLA_ERR_INVALID, "%s: pointer %p is not aligned to its element", what, q);
+  const Span in[] = {{x, n * es}, {residual, n * es}};
+  const Span g{gain, (size_t)M * es};
+  const Span same[] = {{residual_out, n * es}, {out, n * es}};
+  const Span bytes[] = {{codes, n}, {scales, (size_t)T}};
+  bool bad = overlap(same[0], same[1]) || overlap(bytes[0], bytes[1]);
+  for (const Span& o : same) {
+    for (const Span& i : in) bad = bad || overlap_shifted(o, i);
+    for (const Span& b : bytes) bad = bad || overlap(o, b);
+    bad = bad || overlap(o, g);
+  }
+  for (const Span& b : bytes) {
+    for (const Span& i : in) bad = bad || overlap(b, i);
+    bad = bad || overlap(b, g);
+  }
+  if (bad) return fail(MLA_ERR_INVALID, "%s: an output overlaps another operand", what);
+  mla::rms::Params p;
+  p.x = x;
+  p.r = residual;
+  p.gain = gain;
+  p.r_out = residual_out;
+  p.y = out;
+  p.codes = static_cast<uint8_t*>(codes);
+  p.scales = static_cast<uint8_t*>(scales);
+  p.T = T;
+  p.M = M;
+  p.eps = eps;
+  return dtype == MLA_BF16 ? launch_rms<__nv_bfloat16>(p, as_stream(stream)) : launch_rms<float>(p, as_stream(stream));
+}
+
+// ------------------------------------------------------------------------------- projections
+mla_status linear(const char* what, bool f8, const void* x, const void* xs, const void* W, const void* ws,
+                  const void* bias, const void* mul, const void* residual, void* out, int32_t T, int32_t N, int32_t K,
+                  int32_t act, void* stream) {
+  if (T < 0 || N <= 0 || K <= 0) return fail(MLA_ERR_INVALID, "%s: bad sizes T=%d N=%d K=%d", what, T, N, K);
+  if (act < MLA_ACT_NONE || act > MLA_ACT_GELU) return fail(MLA_ERR_INVALID, "%s: unknown activation %d", what, act);
+  if (T == 0) return ok();
+  if (!x || !W || !out || (f8 && (!xs || !ws))) return fail(MLA_ERR_INVALID, "%s: null pointer", what);
+  for (const void* q : {f8 ? nullptr : x, f8 ? nullptr : W, bias, mul, residual, (const void*)out})
+    if (reinterpret_cast<uintptr_t>(q) % 2 != 0)
+      return fail(MLA_ERR_INVALID, "%s: pointer %p is not aligned to its element", what, q);
+  const size_t es = f8 ? 1 : 2, tn = (size_t)T * N * 2;
+  const Span o{out, tn};
+  if (overlap(o, {x, (size_t)T * K * es}) || overlap(o, {W, (size_t)N * K * es}) || overlap(o, {bias, (size_t)N * 2}) ||
+      overlap(o, {xs, (size_t)T}) || overlap(o, {ws, (size_t)N}) || overlap_shifted(o, {mul, tn}) ||
+      overlap_shifted(o, {residual, tn}))
+    return fail(MLA_ERR_INVALID, "%s: out overlaps another operand", what);
+  mla::lin::Params p;
+  p.bias = static_cast<const __nv_bfloat16*>(bias);
+  p.mul = static_cast<const __nv_bfloat16*>(mul);
+  p.res = static_cast<const __nv_bfloat16*>(residual);
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.xs = static_cast<const uint8_t*>(xs);
+  p.ws = static_cast<const uint8_t*>(ws);
+  p.T = T;
+  p.N = N;
+  p.K = K;
+  p.act = act;
+  p.timeout_ns = g_timeout_ns.load();
+  cudaStream_t st = as_stream(stream);
+  const int64_t blocks = (((int64_t)T + mla::lin::kTile - 1) / mla::lin::kTile) * (((int64_t)N + mla::lin::kTile - 1) / mla::lin::kTile);
+  if (blocks > 0x7FFFFFFF) return fail(MLA_ERR_UNSUPPORTED, "%s: T=%d N=%d is too large", what, T, N);
+  if (f8) mla::lin::linear_simt_kernel<true><<<(unsigned)blocks, 256, 0, st>>>(x, W, p);
+  else mla::lin::linear_simt_kernel<false><<<(unsigned)blocks, 256, 0, st>>>(x, W, p);
+  return launch_check(what);
+}
+
+}  // namespace
+
+extern "C" {
+
+mla_status mla_add_rmsnorm(const void* x, const void* residual, const void* gain, void* residual_out, void* out,
+                           int32_t T, int32_t M, float eps, int32_t dtype, void* stream) {
+  return add_rmsnorm("add_rmsnorm", x, residual, gain, residual_out, out, nullptr, nullptr, T, M, eps, dtype, false,
+                     stream);
+}
+
+mla_status mla_add_rmsnorm_fp8(const void* x, const void* residual, const void* gain, void* residual_out, void* out,
+                               void* codes, void* scales, int32_t T, int32_t M, float eps, int32_t dtype,
+                               void* stream) {
+  return add_rmsnorm("add_rmsnorm_fp8", x, residual, gain, residual_out, out, codes, scales, T, M, eps, dtype, true,
+                     stream);
+}
+
+mla_status mla_quantize_fp8(const void* rows, void* codes, void* scales, int32_t n, int32_t width, int32_t dtype,
+                            void* stream) {
+  if (n < 0 || width <= 0) return fail(MLA_ERR_INVALID, "quantize_fp8: bad sizes n=%d width=%d", n, width);
+  if (dtype != MLA_BF16 && dtype != MLA_F32)
+    return fail(MLA_ERR_INVALID, "quantize_fp8: dtype must be MLA_BF16 or MLA_F32, got %d", dtype);
+  if (n == 0) return ok();
+  if (!rows || !codes || !scales) return fail(MLA_ERR_INVALID, "quantize_fp8: null pointer");
+  const size_t es = dtype == MLA_BF16 ? 2 : 4, m = (size_t)n * width;
+  if (reinterpret_cast<uintptr_t>(rows) % es != 0)
+    return fail(MLA_ERR_INVALID, "quantize_fp8: pointer %p is not aligned to its element", rows);
+  const Span in{rows, m * es}, c{codes, m}, sc{scales, (size_t)n};
+  if (overlap(c, in) || overlap(sc, in) || overlap(c, sc))
+    return fail(MLA_ERR_INVALID, "quantize_fp8: an output overlaps another operand");
+  mla::rms::Params p{};
+  p.x = rows;
+  p.codes = static_cast<uint8_t*>(codes);
+  p.scales = static_cast<uint8_t*>(scales);
+  p.T = n;
+  p.M = width;
+  return dtype == MLA_BF16 ? launch_rms<__nv_bfloat16>(p, as_stream(stream)) : launch_rms<float>(p, as_stream(stream));
+}
+
+mla_status mla_linear(const void* x, const void* W, const void* bias, const void* mul, const void* residual, void* out,
+                      int32_t T, int32_t N, int32_t K, int32_t act, void* stream) {
+  return linear("linear", false, x, nullptr, W, nullptr, bias, mul, residual, out, T, N, K, act, stream);
+}
+
+mla_status mla_linear_fp8(const void* x_codes, const void* x_scales, const void* W_codes, const void* W_scales,
+                          const void* bias, const void* mul, const void* residual, void* out, int32_t T, int32_t N,
+                          int32_t K, int32_t act, void* stream) {
+  return linear("linear_fp8", true, x_codes, x_scales, W_codes, W_scales, bias, mul, residual, out, T, N, K, act,
+                stream);
 }
 
 }  // extern "C"

@@ -23,6 +23,7 @@ Modules:
   loops       a scalar pure-Python restatement for tiny brute-force cases.
   ledger      the per-token KV-state byte ledger.
   fp8         the 8-bit (E4M3) cache: rounding, codes, per-token power-of-two scales.
+  layer       the residual's addition and RMS norm, the projections with their epilogue.
 
 Every function here is pinned by a ``-m "not gpu"`` test in tests/test_oracle.py
 against something other than itself (closed forms, a library routine, brute force,

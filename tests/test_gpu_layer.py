@@ -1,0 +1,376 @@
+"""GPU parity of the layer's operators around the attention with their fp64 oracle.
+
+Tolerances, from the arithmetic. A store rounds by at most half a step: 2^-8 of the value in
+bf16, 2^-24 in fp32, 2^-4 in E4M3 (or half its subnormal step, 2^-10 of the row's scale).
+The norm's fp32 statistics: a sum of M squares in a tree of at most 16 terms a thread and 10
+levels, halved by the square root, and five further roundings: below 2^-18 relative.
+Projections: on integers whose sums stay below 2^24 every fp32 step is exact and the output
+must equal the rounded exact value bit for bit; on random values K additions err by at most
+2^-23 of sum |x w| each, an activation passes an error on by at most 1.13 times and adds
+2^-20 of its value.
+"""
+import numpy as np
+import pytest
+import torch
+
+import mla_latent_kv_46_b200 as mla
+from mla_latent_kv_46_b200 import decoder as dec
+from inputs import workloads as wl
+from oracle import fp8, layer
+from oracle import mla_oracle as orc
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+GUARD = 64      # elements on either side of an output that must keep their value
+STAT = 2.0 ** -18
+ACT = {"none": mla.MLA_ACT_NONE, "sigmoid": mla.MLA_ACT_SIGMOID, "silu": mla.MLA_ACT_SILU, "gelu": mla.MLA_ACT_GELU}
+POLICIES = {"auto": mla.MLA_POLICY_AUTO, "simt": mla.MLA_POLICY_SIMT}
+
+
+@pytest.fixture(autouse=True)
+def _reset():
+    yield
+    mla.mla_set_policy(mla.MLA_POLICY_AUTO)
+    mla.mla_check_status()
+
+
+def host(t):
+    return t.detach().double().cpu().numpy()
+
+
+class Guarded:
+    """A contiguous output tensor with guard elements before and after it. `shift`: the
+    tensor starts that many elements past an aligned address."""
+
+    def __init__(self, shape, dtype, shift=0):
+        n = int(np.prod(shape))
+        self.n, self.at = n, GUARD + shift
+        self.whole = torch.full((n + 2 * GUARD + shift,), 77, dtype=dtype, device=DEV)
+        self.t = self.whole[self.at:self.at + n].view(*shape)
+
+    def check(self):
+        assert bool((self.whole[:self.at] == 77).all()) and bool((self.whole[self.at + self.n:] == 77).all())
+
+
+def shifted(t, shift):
+    """t's values in a contiguous tensor that starts `shift` elements past an aligned address."""
+    if shift == 0:
+        return t
+    whole = torch.empty(t.numel() + shift, dtype=t.dtype, device=t.device)
+    whole[shift:] = t.reshape(-1)
+    return whole[shift:].view(t.shape)
+
+
+# ----------------------------------------------------------------------------- residual add + RMS norm
+def norm_inputs(T, M, dtype, seed=0, residual=True):
+    g = torch.Generator(device="cpu").manual_seed(seed)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    x = torch.randn(T, M, generator=g).to(dt).to(DEV)
+    loud = 1 + 20 * (torch.rand(M, generator=g) < 0.02)
+    r = (torch.randn(T, M, generator=g) * loud).to(dt).to(DEV) if residual else None
+    gain = (1 + 0.3 * torch.randn(M, generator=g)).to(dt).to(DEV)
+    return x, r, gain
+
+
+def check_rounded(got, ref, half, what):
+    err = np.abs(got - ref)
+    bound = (half + STAT) * np.abs(ref) + 1e-30
+    assert np.all(err <= bound), f"{what}: worst {np.max(err / bound):.3f} of the bound"
+
+
+def check_codes(codes, scales, y, what=""):
+    """The scale is the smallest power of two the row fits (up to the statistics' error) and
+    every code is the nearest to its value (within it)."""
+    c, k = codes.cpu().numpy(), scales.cpu().numpy().astype(np.int64) - 127
+    amax = np.abs(y).max(axis=1)
+    assert np.all((amax * (1 - STAT) <= np.ldexp(448.0, k)) | (k == 7)), what
+    assert np.all((amax * (1 + STAT) > np.ldexp(448.0, k - 1)) | (k == -126)), what
+    val = fp8.dequantise_rows(c, (k + 127).astype(np.uint8))
+    top = np.ldexp(448.0, k)[:, None]
+    yc = np.clip(y, -top, top)
+    bound = (2.0 ** -4 + STAT) * np.abs(yc) * (1 + STAT)
+    bound = np.maximum(bound, np.ldexp(1.0, k - 10)[:, None] * (1 + STAT))
+    assert np.all(np.abs(val - yc) <= bound), what
+
+
+def run_norm(x, r, gain, T, M, dtype, codes, with_y=True, shift=0, eps=1e-6):
+    dt = x.dtype
+    dtype = mla.MLA_BF16 if dtype == "bf16" else mla.MLA_F32
+    ro = Guarded((T, M), dt, shift) if r is not None else None
+    y = Guarded((T, M), dt, shift) if with_y else None
+    c = Guarded((T, M), torch.uint8, shift) if codes else None
+    s = Guarded((T,), torch.uint8, shift) if codes else None
+    t = lambda v: None if v is None else v.t  # noqa: E731
+    if codes:
+        mla.mla_add_rmsnorm_fp8(x, r, gain, t(ro), t(y), c.t, s.t, T, M, eps, dtype)
+    else:
+        mla.mla_add_rmsnorm(x, r, gain, t(ro), y.t, T, M, eps, dtype)
+    torch.cuda.synchronize()
+    for v in (ro, y, c, s):
+        if v is not None:
+            v.check()
+    return t(ro), t(y), t(c), t(s)
+
+
+NORM_SHAPES = [(1, 1), (3, 2), (2, 8), (5, 31), (1, 64), (7, 96), (33, 255), (9, 256), (5, 257), (4, 512), (3, 1000),
+               (2, 1111), (129, 1536), (2, 4100), (1, 7168), (150, 7168), (2, 8192), (2, 8200), (3, 12290), (1, 16384),
+               (2, 16385), (1, 20000), (1, 40001)]
+
+
+@pytest.mark.parametrize("codes", [False, True], ids=["plain", "codes"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,M", NORM_SHAPES)
+def test_add_rmsnorm_matches_oracle(T, M, dtype, codes):
+    x, r, gain = norm_inputs(T, M, dtype, seed=T + M)
+    ro, y, c, s = run_norm(x, r, gain, T, M, dtype, codes)
+    ref_s, ref_y = layer.add_rmsnorm(host(x), host(r), host(gain), 1e-6)
+    half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    check_rounded(host(ro), ref_s, half, "residual")
+    check_rounded(host(y), ref_y, half, "y")
+    if codes:
+        check_codes(c, s, ref_y)
+
+
+@pytest.mark.parametrize("shift", [1, 2, 4])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_add_rmsnorm_at_any_alignment(dtype, shift):
+    T, M = 5, 520
+    x, r, gain = norm_inputs(T, M, dtype, seed=shift)
+    ro, y, c, s = run_norm(shifted(x, shift), shifted(r, shift), shifted(gain, shift), T, M, dtype, True, shift=shift)
+    a_ro, a_y, a_c, a_s = run_norm(x, r, gain, T, M, dtype, True)
+    ref_s, ref_y = layer.add_rmsnorm(host(x), host(r), host(gain), 1e-6)
+    half = 2.0 ** -8 if dtype == "bf16" else 2.0 ** -24
+    check_rounded(host(ro), ref_s, half, "residual")
+    check_rounded(host(y), ref_y, half, "y")
+    check_codes(c, s, ref_y)
+    assert torch.equal(ro, a_ro)
+
+
+@pytest.mark.parametrize("T,M", [(3, 200), (2, 7168), (2, 16400)])
+def test_add_rmsnorm_without_residual_and_codes_alone(T, M):
+    x, _, gain = norm_inputs(T, M, "bf16", seed=9, residual=False)
+    _, y, c, s = run_norm(x, None, gain, T, M, "bf16", True, with_y=False)
+    assert y is None
+    check_codes(c, s, layer.add_rmsnorm(host(x), None, host(gain), 1e-6)[1])
+
+
+@pytest.mark.parametrize("M", [96, 1111, 7168, 20000])
+def test_add_rmsnorm_in_place(M):
+    """residual_out on residual and out on x, and the two swapped: bitwise the same."""
+    T = 6
+    x, r, gain = norm_inputs(T, M, "bf16", seed=M)
+    ro, y, _, _ = run_norm(x, r, gain, T, M, "bf16", False)
+    a, b = x.clone(), r.clone()
+    mla.mla_add_rmsnorm(a, b, gain, b, a, T, M, 1e-6, mla.MLA_BF16)
+    assert torch.equal(a, y) and torch.equal(b, ro)
+    a, b = x.clone(), r.clone()
+    mla.mla_add_rmsnorm(a, b, gain, a, b, T, M, 1e-6, mla.MLA_BF16)
+    assert torch.equal(a, ro) and torch.equal(b, y)
+
+
+@pytest.mark.parametrize("M", [64, 1111, 7168, 20000])
+def test_add_rmsnorm_special_rows(M):
+    """Zero rows, tiny and huge rows, and rows with an infinity or a NaN: no other row moves."""
+    x, r, gain = norm_inputs(8, M, "f32", seed=4)
+    _, base, bc, bs = run_norm(x, r, gain, 8, M, "f32", True)
+    x2, r2 = x.clone(), r.clone()
+    x2[1], r2[1] = 0, 0
+    x2[2, M // 2] = float("inf")
+    x2[3, M - 1] = float("nan")
+    x2[4], r2[4] = x[4] * 1e-20, 0
+    x2[5], r2[5] = x[5] * 1e15, 0
+    ro, y, c, s = run_norm(x2, r2, gain, 8, M, "f32", True)
+    for row in (0, 6, 7):
+        assert torch.equal(y[row], base[row]) and torch.equal(c[row], bc[row]) and s[row] == bs[row]
+    assert bool((y[1] == 0).all()) and bool(((c[1] & 0x7F) == 0).all()) and s[1] == 1
+    want = torch.zeros(M, device=DEV)
+    want[M // 2] = float("nan")        # inf / inf; the others finite / inf
+    assert torch.equal(torch.isnan(y[2]), torch.isnan(want)) and bool((y[2][~torch.isnan(want)] == 0).all())
+    assert bool(torch.isnan(y[3]).all())
+    assert bool(((c[3] & 0x7F) == 0x7F).all())
+    ref = layer.add_rmsnorm(host(x2[4:6]), host(r2[4:6]), host(gain), 1e-6)[1]
+    check_rounded(host(y[4:6]), ref, 2.0 ** -24, "y")
+    check_codes(c[4:6], s[4:6], ref)
+
+
+def test_add_rmsnorm_zero_row_without_eps_is_nan():
+    x, _, gain = norm_inputs(2, 64, "bf16", residual=False)
+    x[0] = 0
+    _, y, _, _ = run_norm(x, None, gain, 2, 64, "bf16", False, eps=0.0)
+    assert bool(torch.isnan(y[0]).all()) and bool(torch.isfinite(y[1]).all())
+
+
+# ----------------------------------------------------------------------------- the quantiser
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,width", [(1, 1), (3, 17), (9, 576), (5, 1000), (2, 7168), (2, 16383), (1, 33000)])
+def test_quantize_fp8_is_bit_exact(n, width, dtype):
+    """No arithmetic but the scaling by a power of two comes before the rounding, so codes and
+    scale bytes equal the oracle's for every row, tiny, huge and tied values among them."""
+    rng = np.random.default_rng(width)
+    rows = rng.standard_normal((n, width)) * np.ldexp(1.0, rng.integers(-30, 12, size=(n, 1)))
+    rows[:, ::7] = np.ldexp(np.round(np.ldexp(rows[:, ::7], 6)) + 0.5, -6)
+    t = torch.from_numpy(rows).to(torch.bfloat16 if dtype == "bf16" else torch.float32).to(DEV)
+    c, s = Guarded((n, width), torch.uint8), Guarded((n,), torch.uint8)
+    mla.mla_quantize_fp8(t, c.t, s.t, n, width, mla.MLA_BF16 if dtype == "bf16" else mla.MLA_F32)
+    torch.cuda.synchronize()
+    want_c, want_s = fp8.quantise_rows(host(t))
+    assert np.array_equal(s.t.cpu().numpy(), want_s)
+    assert np.array_equal(c.t.cpu().numpy(), want_c)
+    c.check(), s.check()
+
+
+def test_quantize_fp8_boundaries_and_special_rows():
+    tiny = 2.0 ** -126 * 448
+    rows = torch.tensor([[448.0, 1], [448.0 * 1.001, 1], [0.0, -0.0], [tiny, 0], [tiny / 64, 0], [448.0 * 128, 1],
+                         [448.0 * 200, 1], [float("inf"), 1.0], [float("nan"), 3.0], [0.875, 0.4375]],
+                        dtype=torch.float32, device=DEV)
+    n = rows.shape[0]
+    c = torch.zeros(n, 2, dtype=torch.uint8, device=DEV)
+    s = torch.zeros(n, dtype=torch.uint8, device=DEV)
+    mla.mla_quantize_fp8(rows, c, s, n, 2, mla.MLA_F32)
+    finite = [0, 1, 2, 3, 4, 5, 6, 9]
+    want_c, want_s = fp8.quantise_rows(host(rows)[finite])
+    assert np.array_equal(s.cpu().numpy()[finite], want_s)
+    assert np.array_equal(c.cpu().numpy()[finite], want_c)
+    assert s[7] == 134 and c[7, 0] == 0x7E          # an infinity saturates at the largest scale
+    assert (c[8, 0] & 0x7F) == 0x7F and s[8] == fp8.quantise_rows(np.array([[3.0]]))[1][0]
+
+
+# ----------------------------------------------------------------------------- projections
+def ints(rng, lo, hi, *shape):
+    return rng.integers(lo, hi + 1, size=shape).astype(np.float64)
+
+
+def bf16(a):
+    return torch.from_numpy(a).to(torch.bfloat16).to(DEV)
+
+
+def run_linear(x, W, bias, mul, res, T, N, K, act="none", scales=None, shift=0):
+    out = Guarded((T, N), torch.bfloat16, shift)
+    if scales is None:
+        mla.mla_linear(x, W, bias, mul, res, out.t, T, N, K, ACT[act])
+    else:
+        mla.mla_linear_fp8(x, scales[0], W, scales[1], bias, mul, res, out.t, T, N, K, ACT[act])
+    torch.cuda.synchronize()
+    mla.mla_check_status()
+    out.check()
+    return out.t
+
+
+LIN_SHAPES = [(1, 1, 1), (1, 8, 16), (1, 128, 64), (2, 129, 72), (1, 300, 4096), (3, 1000, 1111), (15, 64, 80),
+              (16, 256, 512), (17, 127, 1008), (31, 1111, 328), (33, 130, 2048), (64, 640, 576), (65, 257, 1000),
+              (127, 200, 96), (128, 512, 4096), (129, 385, 640), (200, 136, 16), (255, 128, 208), (256, 1024, 1024),
+              (257, 1025, 520), (300, 77, 33), (511, 513, 1104), (777, 1111, 1000), (1030, 900, 64), (2500, 300, 264)]
+
+
+def exact_case(T, N, K, eight, epilogue, policy, shift=0):
+    rng = np.random.default_rng(T * 7919 + N * 31 + K)
+    x, W = ints(rng, -4, 4, T, K), ints(rng, -3, 3, N, K)
+    bias = ints(rng, -9, 9, N) if epilogue else None
+    mul = ints(rng, -3, 3, T, N) if epilogue else None
+    res = ints(rng, -99, 99, T, N) if epilogue else None
+    dev = lambda a: None if a is None else shifted(bf16(a), shift)  # noqa: E731
+    mla.mla_set_policy(POLICIES[policy])
+    if eight:
+        kx, kw = rng.integers(-3, 4, size=T), rng.integers(-3, 4, size=N)
+        code = lambda a: shifted(torch.from_numpy(fp8.e4m3_encode(a)).to(DEV), shift)  # noqa: E731
+        byte = lambda k: shifted(torch.from_numpy((k + 127).astype(np.uint8)).to(DEV), shift)  # noqa: E731
+        got = run_linear(code(x), code(W), dev(bias), dev(mul), dev(res), T, N, K, scales=(byte(kx), byte(kw)),
+                         shift=shift)
+        x, W = np.ldexp(x, kx[:, None]), np.ldexp(W, kw[:, None])
+    else:
+        got = run_linear(dev(x), dev(W), dev(bias), dev(mul), dev(res), T, N, K, shift=shift)
+    # the products' sum is an integer below 12 K < 2^16 (times a power of two), and what the
+    # epilogue makes of it has fewer than 24 significant bits: exact in fp32
+    want = orc.round_bf16(layer.linear(x, W, bias, mul, res))
+    assert np.array_equal(host(got), want), f"{np.sum(host(got) != want)} of {want.size} differ"
+
+
+@pytest.mark.parametrize("epilogue", [False, True], ids=["bare", "epilogue"])
+@pytest.mark.parametrize("eight", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("T,N,K", LIN_SHAPES)
+def test_linear_is_exact_on_integers(T, N, K, eight, epilogue):
+    exact_case(T, N, K, eight, epilogue, "auto")
+
+
+@pytest.mark.parametrize("eight", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("T,N,K", [(1, 128, 64), (65, 257, 1000), (130, 70, 48)])
+def test_linear_on_cuda_cores_is_exact_on_integers(T, N, K, eight):
+    exact_case(T, N, K, eight, True, "simt")
+
+
+@pytest.mark.parametrize("eight", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("shift", [1, 8])
+def test_linear_at_any_alignment(shift, eight):
+    exact_case(33, 130, 144, eight, True, "auto", shift=shift)
+
+
+@pytest.mark.parametrize("act", ["none", "sigmoid", "silu", "gelu"])
+@pytest.mark.parametrize("eight", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("T,N,K", [(1, 300, 512), (37, 129, 1000), (200, 257, 640), (600, 520, 1024)])
+def test_linear_matches_oracle_on_random_values(T, N, K, eight, act):
+    rng = np.random.default_rng(T + N + K)
+    x, W = rng.standard_normal((T, K)), rng.standard_normal((N, K)) * 2 / np.sqrt(K)
+    bias, mul, res = bf16(rng.standard_normal(N)), bf16(rng.standard_normal((T, N))), bf16(rng.standard_normal((T, N)))
+    if eight:
+        (cx, sx), (cw, sw) = fp8.quantise_rows(x), fp8.quantise_rows(W)
+        t = [torch.from_numpy(a).to(DEV) for a in (cx, sx, cw, sw)]
+        got = run_linear(t[0], t[2], bias, mul, res, T, N, K, act, scales=(t[1], t[3]))
+        x, W = fp8.dequantise_rows(cx, sx), fp8.dequantise_rows(cw, sw)
+    else:
+        xb, Wb = bf16(x), bf16(W)
+        got = run_linear(xb, Wb, bias, mul, res, T, N, K, act)
+        x, W = host(xb), host(Wb)
+    b, m, r = host(bias), host(mul), host(res)
+    ref = layer.linear(x, W, b, m, r, act)
+    acc = (K + 2) * 2.0 ** -23 * (np.abs(x) @ np.abs(W).T + np.abs(b))
+    part = np.abs(m) * (1.13 * acc + 2.0 ** -20 * np.abs(layer.activation(x @ W.T + b, act)))
+    bound = 2.0 ** -8 * np.abs(ref) + (1 + 2.0 ** -8) * (part + 2.0 ** -22 * np.abs(r)) + 1e-30
+    err = np.abs(host(got) - ref)
+    assert np.all(err <= bound), f"worst {np.max(err / bound):.3f} of the bound"
+
+
+@pytest.mark.parametrize("T,N,K", [(5, 200, 512), (300, 520, 640)])
+def test_linear_in_place_on_its_residual_and_on_mul(T, N, K):
+    rng = np.random.default_rng(5)
+    x, W, m, r = (bf16(rng.standard_normal(s)) for s in ((T, K), (N, K), (T, N), (T, N)))
+    want = run_linear(x, W, None, m, r, T, N, K, "sigmoid")
+    a = r.clone()
+    mla.mla_linear(x, W, None, m, a, a, T, N, K, mla.MLA_ACT_SIGMOID)
+    b = m.clone()
+    mla.mla_linear(x, W, None, b, r, b, T, N, K, mla.MLA_ACT_SIGMOID)
+    torch.cuda.synchronize()
+    assert torch.equal(a, want) and torch.equal(b, want)
+
+
+@pytest.mark.parametrize("T,N,K", [(3, 140, 256), (260, 140, 256)])
+def test_linear_keeps_a_rows_nan_and_infinity_in_that_row(T, N, K):
+    rng = np.random.default_rng(6)
+    x, W = bf16(rng.standard_normal((T, K))), bf16(rng.standard_normal((N, K)))
+    want = run_linear(x, W, None, None, None, T, N, K)
+    y = x.clone()
+    y[1, 3] = float("nan")
+    y[2, K - 1] = float("inf")
+    got = run_linear(y, W, None, None, None, T, N, K)
+    keep = [t for t in range(T) if t not in (1, 2)]
+    assert torch.equal(got[keep], want[keep])
+    assert bool(torch.isnan(got[1]).all()) and not bool(torch.isfinite(got[2]).any())
+
+
+@pytest.mark.parametrize("act,lo,hi", [("sigmoid", 0.0, 1.0), ("silu", 0.0, 3e4), ("gelu", 0.0, 3e4)])
+def test_linear_activations_at_their_ends(act, lo, hi):
+    """Sums of -30000 and +30000: no overflow, no NaN."""
+    x = bf16(np.array([[-3e4], [3e4]] * 1).repeat(16, axis=1) / 16)
+    W = bf16(np.ones((8, 16)))
+    got = host(run_linear(x, W, None, None, None, 2, 8, 16, act))
+    v = float(bf16(np.array([3e4 / 16]))[0]) * 16
+    assert np.all(got[0] == lo) and np.all(np.abs(got[1] - (1.0 if act == "sigmoid" else v)) <= 2.0 ** -8 * v)
+
+
+def test_two_runs_are_bitwise_equal():
+    rng = np.random.default_rng(8)
+    for T, N, K in ((1, 7168, 2048), (37, 2000, 4096), (700, 1111, 1000)):
+        x, W = bf16(rng.standard_normal((T, K))), bf16(rng.standard_normal((N, K)))
+        a = run_linear(x, W, None, None, None, T, N, K)
+        assert torch.equal(a, run_linear(x, W, None, None, None, T, N, K))
