@@ -28,6 +28,7 @@
 #include "prefill.cuh"
 #include "add_rmsnorm.cuh"
 #include "linear.cuh"
+#include "linear_tc.cuh"
 
 namespace {
 
@@ -1343,6 +1344,81 @@ mla_status add_rmsnorm(const char* what, const void* x, const void* residual, co
 }
 
 // ------------------------------------------------------------------------------- projections
+int32_t device_sms() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return sms;
+}
+
+// Tensor maps of W (boxes of `w_rows` rows) and x (`x_rows` rows), 128 bytes of K wide.
+template <bool F8>
+mla_status linear_maps(CUtensorMap* tw, CUtensorMap* tx, const void* W, const void* x, const mla::lin::Params& p,
+                       uint32_t w_rows, uint32_t x_rows) {
+  const uint64_t K = (uint64_t)p.K;
+  if (F8) {
+    if (mla_status s = make_map_u8_2d(tw, W, K, (uint64_t)p.N, K, w_rows)) return s;
+    return make_map_u8_2d(tx, x, K, (uint64_t)p.T, K, x_rows);
+  }
+  if (mla_status s = make_map_2d(tw, W, K, (uint64_t)p.N, K * 2, w_rows)) return s;
+  return make_map_2d(tx, x, K, (uint64_t)p.T, K * 2, x_rows);
+}
+
+template <bool F8, int NT, int STAGES>
+mla_status launch_linear_split(const void* x, const void* W, const mla::lin::Params& p, int32_t sms, cudaStream_t st,
+                               const char* what) {
+  using C = mla::lin::SplitCfg<F8, NT, STAGES>;
+  auto kern = mla::lin::linear_split_kernel<F8, NT, STAGES>;
+  CUtensorMap tw, tx;
+  if (mla_status s = linear_maps<F8>(&tw, &tx, W, x, p, mla::lin::kM, NT)) return s;
+  if (mla_status s = ensure_smem_attr((const void*)kern, C::kSmemBytes)) return s;
+  const int64_t tiles_n = ((int64_t)p.N + mla::lin::kM - 1) / mla::lin::kM, tiles_t = ((int64_t)p.T + NT - 1) / NT;
+  const int kblk = (p.K + mla::lin::kb_elems<F8>() - 1) / mla::lin::kb_elems<F8>();
+  // K slices: as many CTAs as the GPU holds at once (two per SM where shared memory allows)
+  const int64_t room = (int64_t)sms * (C::kSmemBytes <= 113 * 1024 ? 2 : 1);
+  const int slices = (int)std::max<int64_t>(1, std::min<int64_t>({room / (tiles_n * tiles_t), 8, (kblk + 1) / 2}));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)slices, (unsigned)tiles_n, (unsigned)tiles_t);
+  cfg.blockDim = dim3(128);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)slices;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  MLA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, tw, tx, p));
+  return launch_check(what);
+}
+
+template <bool F8, int NT, int STAGES>
+mla_status launch_linear_pair(const void* x, const void* W, const mla::lin::Params& p, int32_t sms, cudaStream_t st,
+                              const char* what) {
+  using C = mla::lin::PairCfg<F8, NT, STAGES>;
+  auto kern = mla::lin::linear_pair_kernel<F8, NT, STAGES>;
+  CUtensorMap tw, tx;
+  if (mla_status s = linear_maps<F8>(&tw, &tx, W, x, p, mla::lin::kM, NT / 2)) return s;
+  if (mla_status s = ensure_smem_attr((const void*)kern, C::kSmemBytes)) return s;
+  const int64_t tiles = (((int64_t)p.N + 2 * mla::lin::kM - 1) / (2 * mla::lin::kM)) * (((int64_t)p.T + NT - 1) / NT);
+  const unsigned pairs = (unsigned)std::min<int64_t>(tiles, std::max(1, sms / 2));
+  kern<<<2 * pairs, C::kThreads, C::kSmemBytes, st>>>(tw, tx, p);
+  return launch_check(what);
+}
+
+template <bool F8>
+mla_status linear_tc(const void* x, const void* W, const mla::lin::Params& p, cudaStream_t st, const char* what) {
+  const int32_t sms = device_sms();
+  if (p.T <= 16) return launch_linear_split<F8, 16, 6>(x, W, p, sms, st, what);
+  if (p.T <= 32) return launch_linear_split<F8, 32, 5>(x, W, p, sms, st, what);
+  if (p.T <= 64) return launch_linear_split<F8, 64, 4>(x, W, p, sms, st, what);
+  if (p.T <= 128) return launch_linear_split<F8, 128, 3>(x, W, p, sms, st, what);
+  if (p.T <= 256) return launch_linear_split<F8, 256, 4>(x, W, p, sms, st, what);
+  return launch_linear_pair<F8, 256, 6>(x, W, p, sms, st, what);
+}
+
 mla_status linear(const char* what, bool f8, const void* x, const void* xs, const void* W, const void* ws,
                   const void* bias, const void* mul, const void* residual, void* out, int32_t T, int32_t N, int32_t K,
                   int32_t act, void* stream) {
@@ -1372,6 +1448,15 @@ mla_status linear(const char* what, bool f8, const void* x, const void* xs, cons
   p.act = act;
   p.timeout_ns = g_timeout_ns.load();
   cudaStream_t st = as_stream(stream);
+  // what TMA needs: 16-byte aligned operands and rows; the token and feature tile numbers
+  // within the grid's and the coordinates' 32 bits
+  const int32_t pol = g_policy.load();
+  const bool tc = reinterpret_cast<uintptr_t>(x) % 16 == 0 && reinterpret_cast<uintptr_t>(W) % 16 == 0 &&
+                  (size_t)K * es % 16 == 0 && T <= 0x7FFFF000 && N <= 65535 * mla::lin::kM;
+  if (pol == MLA_POLICY_TCGEN05 && !tc)
+    return fail(MLA_ERR_UNSUPPORTED, "%s: the tensor-core kernels need 16-byte aligned rows of x and W", what);
+  if (pol != MLA_POLICY_SIMT && tc)
+    return f8 ? linear_tc<true>(x, W, p, st, what) : linear_tc<false>(x, W, p, st, what);
   const int64_t blocks = (((int64_t)T + mla::lin::kTile - 1) / mla::lin::kTile) * (((int64_t)N + mla::lin::kTile - 1) / mla::lin::kTile);
   if (blocks > 0x7FFFFFFF) return fail(MLA_ERR_UNSUPPORTED, "%s: T=%d N=%d is too large", what, T, N);
   if (f8) mla::lin::linear_simt_kernel<true><<<(unsigned)blocks, 256, 0, st>>>(x, W, p);

@@ -261,7 +261,8 @@ def run_linear(x, W, bias, mul, res, T, N, K, act="none", scales=None, shift=0):
 LIN_SHAPES = [(1, 1, 1), (1, 8, 16), (1, 128, 64), (2, 129, 72), (1, 300, 4096), (3, 1000, 1111), (15, 64, 80),
               (16, 256, 512), (17, 127, 1008), (31, 1111, 328), (33, 130, 2048), (64, 640, 576), (65, 257, 1000),
               (127, 200, 96), (128, 512, 4096), (129, 385, 640), (200, 136, 16), (255, 128, 208), (256, 1024, 1024),
-              (257, 1025, 520), (300, 77, 33), (511, 513, 1104), (777, 1111, 1000), (1030, 900, 64), (2500, 300, 264)]
+              (257, 1025, 520), (300, 77, 33), (511, 513, 1104), (777, 1111, 1000), (1030, 900, 64), (2500, 300, 264),
+              (5001, 1300, 144)]      # the last: more 256 x 256 tiles than pairs of SMs
 
 
 def exact_case(T, N, K, eight, epilogue, policy, shift=0):
