@@ -1243,47 +1243,88 @@ mla_status mla_decode_attn_noalloc(const void* q_lat, const void* q_rope, const 
 
 namespace {
 
-// The widest power-of-two number of elements, at most `most`, that divides the row and
-// keeps every given pointer's rows aligned to its size.
-int vec_elems(int32_t M, int esize, std::initializer_list<const void*> rows, const void* codes) {
-  for (int ve = 16 / esize; ve > 1; ve /= 2) {
-    bool fits = M % ve == 0 && reinterpret_cast<uintptr_t>(codes) % ve == 0;
-    for (const void* q : rows) fits = fits && reinterpret_cast<uintptr_t>(q) % (size_t)(ve * esize) == 0;
-    if (fits) return ve;
-  }
-  return 1;
+int32_t device_sms() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return sms;
 }
 
-template <typename T, int VE, int EPT>
-mla_status launch_rms_ept(const mla::rms::Params& p, cudaStream_t st) {
-  constexpr int kItems = EPT / VE;
-  const int chunks = p.M / VE;
-  if (chunks <= 32 * kItems) {
+template <typename T, int ITEMS, bool SHIFTED>
+mla_status launch_rms_rows(const mla::rms::Params& p, int granules, cudaStream_t st) {
+  if (granules <= 32 * ITEMS) {
     const unsigned blocks = (unsigned)(((int64_t)p.T + mla::rms::kWarpRows - 1) / mla::rms::kWarpRows);
-    mla::rms::add_rmsnorm_kernel<T, VE, kItems, true><<<blocks, 32 * mla::rms::kWarpRows, 0, st>>>(p);
+    mla::rms::add_rmsnorm_kernel<T, ITEMS, true, SHIFTED><<<blocks, 32 * mla::rms::kWarpRows, 0, st>>>(p);
   } else {
-    const int threads = ((chunks + kItems - 1) / kItems + 31) / 32 * 32;
-    mla::rms::add_rmsnorm_kernel<T, VE, kItems, false><<<(unsigned)p.T, threads, 0, st>>>(p);
+    const int threads = ((granules + ITEMS - 1) / ITEMS + 31) / 32 * 32;
+    mla::rms::add_rmsnorm_kernel<T, ITEMS, false, SHIFTED><<<(unsigned)p.T, threads, 0, st>>>(p);
   }
   return launch_check("add_rmsnorm");
 }
 
-template <typename T, int VE>
-mla_status launch_rms_ve(const mla::rms::Params& p, cudaStream_t st) {
-  if (p.M <= 8 * 1024) return launch_rms_ept<T, VE, 8>(p, st);
-  if (p.M <= 16 * mla::rms::max_threads(16)) return launch_rms_ept<T, VE, 16>(p, st);
-  mla::rms::add_rmsnorm_wide_kernel<T><<<(unsigned)p.T, 1024, 0, st>>>(p);
+// Blocks of the streaming kernel that an SM holds (0: none), asked for once per kernel,
+// block size, shared memory and device.
+int blocks_per_sm(const void* kernel, int threads, int64_t smem) {
+  struct Known {
+    const void* kernel;
+    int threads, dev, blocks;
+    int64_t smem;
+  };
+  static std::mutex mu;
+  static std::vector<Known> known;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> lk(mu);
+  for (const Known& k : known)
+    if (k.kernel == kernel && k.threads == threads && k.smem == smem && k.dev == dev) return k.blocks;
+  int blocks = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, threads, (size_t)smem) != cudaSuccess) blocks = 0;
+  if (known.size() >= 64) known.erase(known.begin());
+  known.push_back({kernel, threads, dev, blocks, smem});
+  return blocks;
+}
+
+template <typename T, bool SHIFTED>
+mla_status launch_rms(const mla::rms::Params& p, cudaStream_t st) {
+  constexpr int VE = mla::rms::granule<T>();
+  const int granules = (int)(mla::rms::stream_row_bytes<T>(p.M) / 16) - (SHIFTED ? 0 : 1);
+  // The streaming kernel takes rows of 2 KiB and more, and wants a few rows per block: with
+  // fewer its ring never fills (T = 512, M = 7168 bf16: 8.3 us either way; T = 1024: 10.4
+  // against 12.5 us; T = 1024, M = 1024: 6.3 against 4.3 us, two rows a block).
+  constexpr int kItems = 32 / VE, kMaxSmem = 220 * 1024;
+  const int64_t smem = mla::rms::stream_smem<T>(p.M, p.r != nullptr);
+  const int threads = ((granules + kItems - 1) / kItems + 31) / 32 * 32;
+  if (p.gain && (int64_t)p.M * sizeof(T) >= 2048 && threads <= mla::rms::kStreamThreads && smem <= kMaxSmem) {
+    auto kern = mla::rms::add_rmsnorm_stream_kernel<T, kItems, SHIFTED>;
+    const int sms = device_sms();
+    if (p.T >= 2 * sms) {
+      if (mla_status s = ensure_smem_attr((const void*)kern, kMaxSmem)) return s;
+      const int64_t resident = (int64_t)sms * blocks_per_sm((const void*)kern, threads, smem);
+      if (resident > 0 && 2 * (int64_t)p.T >= 5 * resident) {
+        kern<<<(unsigned)resident, threads, (size_t)smem, st>>>(p, g_timeout_ns.load());
+        return launch_check("add_rmsnorm");
+      }
+    }
+  }
+  // else the fewest elements a thread that 1024 threads allow
+  if (granules <= 8 / VE * 1024) return launch_rms_rows<T, 8 / VE, SHIFTED>(p, granules, st);
+  if (granules <= 16 / VE * 1024) return launch_rms_rows<T, 16 / VE, SHIFTED>(p, granules, st);
+  mla::rms::add_rmsnorm_any_kernel<T><<<(unsigned)p.T, 1024, 0, st>>>(p);
   return launch_check("add_rmsnorm");
 }
 
 template <typename T>
 mla_status launch_rms(const mla::rms::Params& p, cudaStream_t st) {
-  const int ve = vec_elems(p.M, sizeof(T), {p.x, p.r, p.gain, p.r_out, p.y}, p.codes);
-  if constexpr (sizeof(T) == 2)
-    if (ve == 8) return launch_rms_ve<T, 8>(p, st);
-  if (ve == 4) return launch_rms_ve<T, 4>(p, st);
-  if (ve == 2) return launch_rms_ve<T, 2>(p, st);
-  return launch_rms_ve<T, 1>(p, st);
+  constexpr int VE = mla::rms::granule<T>();
+  bool aligned = reinterpret_cast<uintptr_t>(p.codes) % VE == 0;
+  for (const void* q : {p.x, p.r, p.gain, (const void*)p.r_out, (const void*)p.y})
+    aligned = aligned && reinterpret_cast<uintptr_t>(q) % 16 == 0;
+  if (!aligned) {
+    mla::rms::add_rmsnorm_any_kernel<T><<<(unsigned)p.T, 1024, 0, st>>>(p);
+    return launch_check("add_rmsnorm");
+  }
+  return p.M % VE == 0 ? launch_rms<T, false>(p, st) : launch_rms<T, true>(p, st);
 }
 
 struct Span {
@@ -1344,14 +1385,6 @@ mla_status add_rmsnorm(const char* what, const void* x, const void* residual, co
 }
 
 // ------------------------------------------------------------------------------- projections
-int32_t device_sms() {
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 0;
-  return sms;
-}
-
 // Tensor maps of W (boxes of `w_rows` rows) and x (`x_rows` rows), 128 bytes of K wide.
 template <bool F8>
 mla_status linear_maps(CUtensorMap* tw, CUtensorMap* tx, const void* W, const void* x, const mla::lin::Params& p,

@@ -195,6 +195,16 @@ __device__ __forceinline__ void bulk_load_g2s(uint32_t dst, const void* src, uin
                : "memory");
 }
 
+// Same, with an L2 eviction-priority policy.
+__device__ __forceinline__ void bulk_load_g2s_hint(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar,
+                                                   uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+      : "memory");
+}
+
 // ------------------------------------------------------------------ CTA pairs (tcgen05 cta_group::2)
 // 2D tiled load into this CTA's shared memory whose completion (bytes) is counted on
 // an mbarrier that may live in either CTA of the pair (`bar_cluster` is a

@@ -115,7 +115,9 @@ def run_norm(x, r, gain, T, M, dtype, codes, with_y=True, shift=0, eps=1e-6):
 
 NORM_SHAPES = [(1, 1), (3, 2), (2, 8), (5, 31), (1, 64), (7, 96), (33, 255), (9, 256), (5, 257), (4, 512), (3, 1000),
                (2, 1111), (129, 1536), (2, 4100), (1, 7168), (150, 7168), (2, 8192), (2, 8200), (3, 12290), (1, 16384),
-               (2, 16385), (1, 20000), (1, 40001)]
+               (2, 16385), (1, 20000), (1, 40001),
+               # many rows: the streaming kernel, with rows that are not a multiple of 16 bytes too
+               (1200, 7168), (1111, 7161), (8000, 1030), (3001, 2049), (3000, 4100), (500, 16379), (9001, 1024)]
 
 
 @pytest.mark.parametrize("codes", [False, True], ids=["plain", "codes"])
@@ -192,6 +194,27 @@ def test_add_rmsnorm_special_rows(M):
     ref = layer.add_rmsnorm(host(x2[4:6]), host(r2[4:6]), host(gain), 1e-6)[1]
     check_rounded(host(y[4:6]), ref, 2.0 ** -24, "y")
     check_codes(c[4:6], s[4:6], ref)
+
+
+@pytest.mark.parametrize("M", [7168, 7163])
+def test_add_rmsnorm_many_rows_in_place_and_with_special_rows(M):
+    """The streaming kernel: outputs on their inputs' buffers, and rows with a NaN or an infinity
+    beside rows that share a 16-byte piece with them."""
+    T = 1300
+    x, r, gain = norm_inputs(T, M, "bf16", seed=M)
+    ro, y, c, s = run_norm(x, r, gain, T, M, "bf16", True)
+    a, b = x.clone(), r.clone()
+    mla.mla_add_rmsnorm(a, b, gain, b, a, T, M, 1e-6, mla.MLA_BF16)
+    assert torch.equal(a, y) and torch.equal(b, ro)
+    x2 = x.clone()
+    x2[5, 0] = float("nan")
+    x2[5, M - 1] = float("inf")
+    x2[T - 1, M - 1] = float("inf")
+    ro2, y2, c2, s2 = run_norm(x2, r, gain, T, M, "bf16", True)
+    keep = torch.ones(T, dtype=torch.bool)
+    keep[[5, T - 1]] = False
+    assert torch.equal(y2[keep], y[keep]) and torch.equal(c2[keep], c[keep]) and torch.equal(s2[keep.to(DEV)], s[keep.to(DEV)])
+    assert bool(torch.isnan(y2[5]).all()) and bool(torch.isnan(y2[T - 1, M - 1])) and bool((y2[T - 1, :M - 1] == 0).all())
 
 
 def test_add_rmsnorm_zero_row_without_eps_is_nan():
