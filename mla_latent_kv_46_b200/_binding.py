@@ -115,7 +115,8 @@ def _ptr(x):
 def _stream(s):
     if s is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without a Stream object (0.2 instead of 3 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -262,12 +263,19 @@ def mla_prefill_attn(ckr, q_nope, q_rope, W_UK, W_UV, cu_seqlens, cu_seqlens_hos
 
 
 def _dense(x):
-    """data_ptr of a contiguous tensor (None -> NULL, integers are raw addresses); the
-    calls take row-major buffers only, so a strided view is refused, not misread."""
+    """data_ptr of a contiguous CUDA tensor on the current device (None -> NULL, integers are
+    raw addresses). The calls take row-major buffers of the device they launch on, so a
+    strided view, a host tensor or another device's is refused, not misread."""
     if x is None or isinstance(x, int):
         return x
     if not x.is_contiguous():
         raise MlaError(MLA_ERR_INVALID, "argument", "tensor is not contiguous")
+    device = x.get_device()
+    if device < 0:
+        raise MlaError(MLA_ERR_INVALID, "argument", "tensor is not on a CUDA device")
+    import torch
+    if device != torch.cuda.current_device():
+        raise MlaError(MLA_ERR_INVALID, "argument", f"tensor is on device {device}, not the current one")
     return x.data_ptr()
 
 

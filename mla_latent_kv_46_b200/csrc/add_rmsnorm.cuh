@@ -17,8 +17,8 @@
 // granule tM / VE. x, r, r' and y share that layout; the codes of a granule are VE aligned
 // bytes, for tM - shift is a multiple of VE. A row's first and last granule may hold a
 // neighbour's elements: those are read and ignored, and never written. Only the gain is
-// out of step with a shifted row; its VE elements come out of two of its granules.
-// (With 2-byte accesses instead, a bf16 row of odd width moved at a quarter of the rate.)
+// out of step with a shifted row. (16384 x 1111 bf16: 33 us; with 2-byte accesses instead,
+// as the row's own alignment allows, about 100.)
 #pragma once
 
 #include "common.cuh"
@@ -37,6 +37,7 @@ struct Params {
   uint8_t* codes;         // [T][M] or null
   uint8_t* scales;        // [T], with codes
   int32_t T, M;
+  float inv_m;            // 1 / M
   float eps;
 };
 
@@ -74,52 +75,25 @@ __device__ __forceinline__ uint4 pack(const float (&v)[granule<T>()]) {
   for (int i = 0; i < granule<T>(); ++i) e[i] = from_f32<T>(v[i]);
   return w;
 }
-// Granule i of a tensor of n elements; one that reaches past the tensor (or before it) is
-// filled element by element, zeros outside.
+// Granule i of a row or tensor, of which elements [0, have) exist (VE: all of them); the
+// others are zeros.
 template <typename T>
-__device__ __forceinline__ uint4 load_granule(const void* base, int64_t i, int64_t n) {
+__device__ __forceinline__ uint4 load_granule(const void* base, int64_t i, int have = granule<T>()) {
   constexpr int VE = granule<T>();
-  if (i >= 0 && (i + 1) * VE <= n) return static_cast<const uint4*>(base)[i];
+  if (have >= VE) return static_cast<const uint4*>(base)[i];
   uint4 w = make_uint4(0, 0, 0, 0);
   T* e = reinterpret_cast<T*>(&w);
 #pragma unroll
   for (int k = 0; k < VE; ++k)
-    if (i * VE + k >= 0 && i * VE + k < n) e[k] = static_cast<const T*>(base)[i * VE + k];
+    if (k < have) e[k] = static_cast<const T*>(base)[i * VE + k];
   return w;
 }
-// The VE elements that start VE - shift elements into granules lo, hi (shift < VE, the same
-// for the whole warp).
-template <typename T>
-__device__ __forceinline__ uint4 window(const uint4& lo, const uint4& hi, int shift) {
-  constexpr int VE = granule<T>(), kPerWord = 4 / (int)sizeof(T);
-  const uint32_t w[9] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w, 0u};
-  const int p = VE - shift;
-  uint32_t r[5];
-  switch (p / kPerWord) {
-#define MLA_RMS_CASE(K)                       \
-  case K:                                     \
-    for (int i = 0; i < 5; ++i) r[i] = w[K + i]; \
-    break;
-    MLA_RMS_CASE(0)
-    MLA_RMS_CASE(1)
-    MLA_RMS_CASE(2)
-    MLA_RMS_CASE(3)
-    default:
-      for (int i = 0; i < 5; ++i) r[i] = w[4 + i];
-#undef MLA_RMS_CASE
-  }
-  if (p % kPerWord != 0) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = __funnelshift_r(r[i], r[i + 1], 16);
-  }
-  return make_uint4(r[0], r[1], r[2], r[3]);
-}
-// Granule i of a row-shaped output, elements [first, last) of it only.
-template <typename T>
+// Elements [first, last) of granule i of a row-shaped output (WHOLE: all of them).
+template <typename T, bool WHOLE>
 __device__ __forceinline__ void store_granule(void* base, int64_t i, const float (&v)[granule<T>()], int first,
                                               int last) {
   constexpr int VE = granule<T>();
-  if (first <= 0 && last >= VE) {
+  if (WHOLE) {
     static_cast<uint4*>(base)[i] = pack<T>(v);
   } else {
 #pragma unroll
@@ -128,14 +102,14 @@ __device__ __forceinline__ void store_granule(void* base, int64_t i, const float
   }
 }
 // The codes of v * up, elements [first, last) of granule i.
-template <int VE>
+template <int VE, bool WHOLE>
 __device__ __forceinline__ void store_codes(uint8_t* base, int64_t i, const float (&v)[VE], float up, int first,
                                             int last) {
   uint32_t c[VE / 4];
 #pragma unroll
   for (int k = 0; k < VE; k += 4)
     c[k / 4] = f8::to_e4m3x2(v[k] * up, v[k + 1] * up) | (f8::to_e4m3x2(v[k + 2] * up, v[k + 3] * up) << 16);
-  if (first <= 0 && last >= VE) {
+  if (WHOLE) {
     if constexpr (VE == 8) reinterpret_cast<uint2*>(base)[i] = make_uint2(c[0], c[1]);
     else reinterpret_cast<uint32_t*>(base)[i] = c[0];
   } else {
@@ -170,66 +144,135 @@ struct Row {
   int64_t g0;      // its first granule
   int shift;       // its first element within that granule
   int count;       // granules it touches
-  __device__ __forceinline__ Row(int64_t row, int M) {
+  int tail;        // the granule that reaches past the tensor's end (-1: none), ..
+  int have;        // .. and its elements inside
+  __device__ __forceinline__ Row(int64_t row, int T, int M) {
     const int64_t e0 = row * M;
     g0 = e0 / VE;
     shift = SHIFTED ? (int)(e0 % VE) : 0;
     count = SHIFTED ? (shift + M + VE - 1) / VE : M / VE;
+    have = (shift + M) % VE;
+    tail = SHIFTED && row == T - 1 && have != 0 ? count - 1 : -1;
   }
   // elements [first, last) of its granule c are the row's
-  __device__ __forceinline__ int first(int c) const { return SHIFTED && c == 0 ? shift : 0; }
-  __device__ __forceinline__ int last(int c, int M) const { return SHIFTED ? min(VE, shift + M - c * VE) : VE; }
+  __device__ __forceinline__ int first(int c) const { return c == 0 ? shift : 0; }
+  __device__ __forceinline__ int last(int c, int M) const { return min(VE, shift + M - c * VE); }
+  __device__ __forceinline__ bool whole(int c) const {
+    return !SHIFTED || ((c > 0 || shift == 0) && (c < count - 1 || have == 0));
+  }
+  // granule c of x or r
+  template <typename T>
+  __device__ __forceinline__ uint4 load(const void* base, int c) const {
+    return load_granule<T>(base, g0 + c, SHIFTED && c == tail ? have : VE);
+  }
 };
 
-// s and its statistics, in the order every kernel here uses: v becomes s * gain.
-template <int VE>
-__device__ __forceinline__ void accumulate(float (&v)[VE], const float (&g)[VE], bool norm, int first, int last,
-                                           float& ss, float& am) {
+// The gains of the row's granule c, columns c VE - shift ..: a shifted row's are not aligned,
+// and come one by one (from L1; zeros outside the row).
+template <typename T, bool SHIFTED>
+__device__ __forceinline__ void gains_of(const void* gain, const Row<granule<T>(), SHIFTED>& at, int c, int M,
+                                         float (&g)[granule<T>()]) {
+  constexpr int VE = granule<T>();
+  if (!SHIFTED) {
+    unpack<T>(static_cast<const uint4*>(gain)[c], g);
+  } else {
+    const T* gp = static_cast<const T*>(gain) + (c * VE - at.shift);
+    if (at.whole(c)) {
 #pragma unroll
-  for (int e = 0; e < VE; ++e)
-    if (e >= first && e < last) {
-      ss += v[e] * v[e];
-      if (norm) v[e] *= g[e];
-      am = fmaxf(am, fabsf(v[e]));
+      for (int e = 0; e < VE; ++e) g[e] = to_f32<T>(gp[e]);
+    } else {
+      const int first = at.first(c), last = at.last(c, M);
+#pragma unroll
+      for (int e = 0; e < VE; ++e) g[e] = e >= first && e < last ? to_f32<T>(gp[e]) : 0.f;
     }
+  }
+}
+
+// s into its statistics, in the order every kernel here uses: v becomes s * gain.
+template <int VE>
+__device__ __forceinline__ void accumulate(float (&v)[VE], const float (&g)[VE], bool norm, float& ss, float& am) {
+#pragma unroll
+  for (int e = 0; e < VE; ++e) {
+    ss += v[e] * v[e];
+    if (norm) v[e] *= g[e];
+    am = fmaxf(am, fabsf(v[e]));
+  }
+}
+
+// The two steps of a granule: its s stored and summed (a neighbour's elements count as
+// zeros from here on); its y stored.
+template <typename T, bool SHIFTED>
+__device__ __forceinline__ void first_step(const Params& p, const Row<granule<T>(), SHIFTED>& at, int c,
+                                           float (&v)[granule<T>()], const float (&g)[granule<T>()], bool norm,
+                                           float& ss, float& am) {
+  constexpr int VE = granule<T>();
+  if (at.whole(c)) {
+    if (p.r_out) store_granule<T, true>(p.r_out, at.g0 + c, v, 0, VE);
+  } else {
+    const int first = at.first(c), last = at.last(c, p.M);
+    if (p.r_out) store_granule<T, false>(p.r_out, at.g0 + c, v, first, last);
+#pragma unroll
+    for (int e = 0; e < VE; ++e)
+      if (e < first || e >= last) v[e] = 0.f;
+  }
+  accumulate<VE>(v, g, norm, ss, am);
+}
+template <typename T, bool SHIFTED>
+__device__ __forceinline__ void second_step(const Params& p, const Row<granule<T>(), SHIFTED>& at, int c,
+                                            float (&v)[granule<T>()], float inv, float up) {
+  constexpr int VE = granule<T>();
+#pragma unroll
+  for (int e = 0; e < VE; ++e) v[e] *= inv;
+  if (at.whole(c)) {
+    if (p.y) store_granule<T, true>(p.y, at.g0 + c, v, 0, VE);
+    if (p.codes) store_codes<VE, true>(p.codes, at.g0 + c, v, up, 0, VE);
+  } else {
+    const int first = at.first(c), last = at.last(c, p.M);
+    if (p.y) store_granule<T, false>(p.y, at.g0 + c, v, first, last);
+    if (p.codes) store_codes<VE, false>(p.codes, at.g0 + c, v, up, first, last);
+  }
 }
 
 // Few rows, or short ones: one row per warp (WARP: blocks of kWarpRows rows) or per block,
 // ITEMS granules a thread, granule c of the row in thread c % threads. Straight loads: with
 // as many threads as the row has granules a call of a few rows is one round trip to memory,
-// and a thread's loads are all in flight before the first is used. A thread keeps its
-// elements and their gains, so blocks of 1024 threads hold up to 16 elements a thread.
+// and a thread's loads are all in flight before the first is used. One row a block: blocks
+// that stay and load the next row's granules under this row's exchange were slower (16384 x
+// 1111 bf16 45 against 37 us; 8000 x 1112 fp32 17.5 against 14.8). A thread keeps its
+// elements and their gains, so blocks of 1024 threads hold up to 16 elements a thread, and
+// kWideThreads up to 32.
+constexpr int kWideThreads = 544;   // 16384 elements and a shifted row's one granule more
+__host__ __device__ constexpr int max_threads(int elems) { return elems <= 16 ? 1024 : kWideThreads; }
+
 template <typename T, int ITEMS, bool WARP, bool SHIFTED>
-__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) add_rmsnorm_kernel(const Params p) {
+__global__ void __launch_bounds__(WARP ? 32 * kWarpRows : max_threads(granule<T>() * ITEMS))
+add_rmsnorm_kernel(const Params p) {
   constexpr int VE = granule<T>();
   __shared__ float red[2][32];
   const int nthr = WARP ? 32 : blockDim.x;
   const int tid = WARP ? (threadIdx.x & 31) : threadIdx.x;
   const int64_t row = WARP ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
   if (WARP && row >= p.T) return;
-  const Row<VE, SHIFTED> at(row, p.M);
-  const int64_t n = (int64_t)p.T * p.M;
-  uint4 xw[ITEMS], rw[ITEMS], gw[ITEMS];
+  const Row<VE, SHIFTED> at(row, p.T, p.M);
+  uint4 xw[ITEMS], rw[ITEMS];
+  float g[ITEMS][VE];
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
     const int c = tid + i * nthr;
-    if (c < at.count) xw[i] = load_granule<T>(p.x, at.g0 + c, n);
+    if (c < at.count) xw[i] = at.template load<T>(p.x, c);
   }
   if (p.r) {
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int c = tid + i * nthr;
-      if (c < at.count) rw[i] = load_granule<T>(p.r, at.g0 + c, n);
+      if (c < at.count) rw[i] = at.template load<T>(p.r, c);
     }
   }
   if (p.gain) {
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int c = tid + i * nthr;
-      if (c < at.count) {
-        gw[i] = load_granule<T>(p.gain, c, p.M);
-        if (SHIFTED && at.shift) gw[i] = window<T>(load_granule<T>(p.gain, c - 1, p.M), gw[i], at.shift);
-      }
+      if (c < at.count) gains_of<T, SHIFTED>(p.gain, at, c, p.M, g[i]);
     }
   }
   float v[ITEMS][VE];
@@ -245,77 +288,52 @@ __global__ void __launch_bounds__(WARP ? 32 * kWarpRows : 1024) add_rmsnorm_kern
 #pragma unroll
         for (int e = 0; e < VE; ++e) v[i][e] += r[e];
       }
-      const int first = at.first(c), last = at.last(c, p.M);
-      if (p.r_out) store_granule<T>(p.r_out, at.g0 + c, v[i], first, last);
-      float g[VE] = {};
-      if (p.gain) unpack<T>(gw[i], g);
-      accumulate<VE>(v[i], g, p.gain != nullptr, first, last, ss, am);
+      first_step<T, SHIFTED>(p, at, c, v[i], g[i], p.gain != nullptr, ss, am);
     }
   }
   if (WARP) warp_reduce(ss, am);
   else block_reduce(ss, am, red);
-  const float inv = p.gain ? 1.f / sqrtf(ss / (float)p.M + p.eps) : 1.f;
+  const float inv = p.gain ? rsqrtf(ss * p.inv_m + p.eps) : 1.f;
   const int k = scale_exponent(am * inv);
   const float up = f8::pow2(-k);
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
     const int c = tid + i * nthr;
-    if (c < at.count) {
-#pragma unroll
-      for (int e = 0; e < VE; ++e) v[i][e] *= inv;
-      const int first = at.first(c), last = at.last(c, p.M);
-      if (p.y) store_granule<T>(p.y, at.g0 + c, v[i], first, last);
-      if (p.codes) store_codes<VE>(p.codes, at.g0 + c, v[i], up, first, last);
-    }
+    if (c < at.count) second_step<T, SHIFTED>(p, at, c, v[i], inv, up);
   }
   if (p.codes && tid == 0) p.scales[row] = (uint8_t)(k + 127);
 }
 
-// Many rows: persistent blocks, each with a ring of kStages row buffers in shared memory
-// that bulk copies keep full while the block works on the oldest row. ITEMS granules a
-// thread. One barrier per row: once it has passed, every thread holds its part of the row
-// in registers and the buffer is loaded again. The inputs are read once, so they are loaded
-// with evict-first priority, which leaves L2 to the writes (T = 16384, M = 7168, bf16 with a
-// residual: 160 us against 169 without, and 204 for the kernel above; two buffers and
-// four granules a thread beat three buffers, or two or eight granules).
+// Many rows of whole granules: persistent blocks, each with a ring of kStages row buffers in
+// shared memory that bulk copies keep full while the block works on the oldest row. ITEMS
+// granules a thread, whose gains it keeps for every row. One barrier per row: once it has
+// passed, every thread holds its part of the row in registers and the buffer is loaded
+// again. The inputs are read once, so they are loaded with evict-first priority, which
+// leaves L2 to the writes (T = 16384, M = 7168, bf16 with a residual: 157 us, 6.0 TB/s,
+// against 169 us without, and 204 for the kernel above; two buffers and four granules a
+// thread beat three buffers, or two or eight granules). Shifted rows gained nothing here.
 constexpr int kStages = 2;
 constexpr int kStreamThreads = 512;
 
-// Shared memory of a block, after the alignment of each part: the ring, then the gain with
-// a granule of zeros on either side.
-template <typename T>
-__host__ __device__ constexpr int64_t stream_row_bytes(int64_t M) {
-  return (M + granule<T>() - 1 + granule<T>() - 1) / granule<T>() * 16;   // touched at the worst shift
-}
-template <typename T>
-__host__ __device__ constexpr int64_t stream_smem(int64_t M, bool residual) {
-  return stream_row_bytes<T>(M) * (residual ? 2 : 1) * kStages + stream_row_bytes<T>(M) + 32;
-}
-
-template <typename T, int ITEMS, bool SHIFTED>
+template <typename T, int ITEMS>
 __global__ void __launch_bounds__(kStreamThreads) add_rmsnorm_stream_kernel(const Params p, uint64_t timeout_ns) {
   constexpr int VE = granule<T>();
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(16) uint8_t smem[];     // [kStages][x row, r row]
   __shared__ __align__(8) uint64_t full_bar[kStages];
   __shared__ float red[2][2][kStreamThreads / 32];
   __shared__ int abort_word;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, nthr = blockDim.x, warps = nthr >> 5;
-  const int64_t n = (int64_t)p.T * p.M;
-  const uint32_t row_bytes = (uint32_t)stream_row_bytes<T>(p.M), stage_bytes = p.r ? 2 * row_bytes : row_bytes;
+  const int count = p.M / VE;
+  const uint32_t row_bytes = (uint32_t)count * 16u, stage_bytes = p.r ? 2 * row_bytes : row_bytes;
   const int grid = gridDim.x;
   auto bar = [&](int s) { return ptx::smem_u32(&full_bar[s]); };
-  // one thread: the row's granules that lie wholly inside the tensor
-  auto fetch = [&](int s, int64_t row) {
-    const Row<VE, SHIFTED> at(row, p.M);
-    const int whole = SHIFTED && (at.g0 + at.count) * VE > n ? at.count - 1 : at.count;
-    const uint32_t bytes = (uint32_t)whole * 16u;
+  auto fetch = [&](int s, int64_t row) {       // one thread
     const uint32_t dst = ptx::smem_u32(smem + (size_t)s * stage_bytes);
     const uint64_t policy = ptx::policy_evict_first();
-    ptx::mbar_arrive_expect_tx(bar(s), p.r ? 2 * bytes : bytes);
-    if (bytes) {
-      ptx::bulk_load_g2s_hint(dst, static_cast<const uint4*>(p.x) + at.g0, bytes, bar(s), policy);
-      if (p.r) ptx::bulk_load_g2s_hint(dst + row_bytes, static_cast<const uint4*>(p.r) + at.g0, bytes, bar(s), policy);
-    }
+    ptx::mbar_arrive_expect_tx(bar(s), stage_bytes);
+    ptx::bulk_load_g2s_hint(dst, static_cast<const uint4*>(p.x) + row * count, row_bytes, bar(s), policy);
+    if (p.r)
+      ptx::bulk_load_g2s_hint(dst + row_bytes, static_cast<const uint4*>(p.r) + row * count, row_bytes, bar(s), policy);
   };
   if (tid == 0) {
     abort_word = 0;
@@ -324,38 +342,30 @@ __global__ void __launch_bounds__(kStreamThreads) add_rmsnorm_stream_kernel(cons
     for (int s = 0; s < kStages; ++s)
       if (blockIdx.x + (int64_t)s * grid < p.T) fetch(s, blockIdx.x + (int64_t)s * grid);
   }
-  // the gain: in registers where every row has the same columns, else in shared memory
   uint4 gw[ITEMS];
-  uint4* sg = reinterpret_cast<uint4*>(smem + (size_t)kStages * stage_bytes);   // granule -1 first
-  if (SHIFTED) {
-    for (int i = tid; i < p.M / VE + 3; i += nthr) sg[i] = load_granule<T>(p.gain, i - 1, p.M);
-  } else {
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      const int c = tid + i * nthr;
-      if (c < p.M / VE) gw[i] = static_cast<const uint4*>(p.gain)[c];
-    }
+  for (int i = 0; i < ITEMS; ++i) {
+    const int c = tid + i * nthr;
+    if (c < count) gw[i] = static_cast<const uint4*>(p.gain)[c];
   }
   __syncthreads();
   int s = 0, it = 0;
   uint32_t parity = 0;
   for (int64_t row = blockIdx.x; row < p.T; row += grid, ++it) {
-    const Row<VE, SHIFTED> at(row, p.M);
+    const Row<VE, false> at(row, p.T, p.M);
     const bool ok = ptx::mbar_wait_bounded(bar(s), parity, &abort_word, timeout_ns);
     const uint4* sx = reinterpret_cast<const uint4*>(smem + (size_t)s * stage_bytes);
-    const uint4* sr = reinterpret_cast<const uint4*>(smem + (size_t)s * stage_bytes + row_bytes);
+    const uint4* sr = sx + count;
     float v[ITEMS][VE];
     float ss = 0.f, am = 0.f;
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int c = tid + i * nthr;
-      if (c < at.count) {
-        // the tensor's last granule, if partial, was not copied
-        const bool tail = SHIFTED && (at.g0 + c + 1) * VE > n;
-        unpack<T>(tail ? load_granule<T>(p.x, at.g0 + c, n) : sx[c], v[i]);
+      if (c < count) {
+        unpack<T>(sx[c], v[i]);
         if (p.r) {
           float r[VE];
-          unpack<T>(tail ? load_granule<T>(p.r, at.g0 + c, n) : sr[c], r);
+          unpack<T>(sr[c], r);
 #pragma unroll
           for (int e = 0; e < VE; ++e) v[i][e] += r[e];
         }
@@ -364,13 +374,10 @@ __global__ void __launch_bounds__(kStreamThreads) add_rmsnorm_stream_kernel(cons
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int c = tid + i * nthr;
-      if (c < at.count) {
-        const int first = at.first(c), last = at.last(c, p.M);
-        if (p.r_out) store_granule<T>(p.r_out, at.g0 + c, v[i], first, last);
+      if (c < count) {
         float g[VE];
-        if (SHIFTED) unpack<T>(at.shift ? window<T>(sg[c], sg[c + 1], at.shift) : sg[c + 1], g);
-        else unpack<T>(gw[i], g);
-        accumulate<VE>(v[i], g, true, first, last, ss, am);
+        unpack<T>(gw[i], g);
+        first_step<T, false>(p, at, c, v[i], g, true, ss, am);
       }
     }
     warp_reduce(ss, am);
@@ -394,19 +401,13 @@ __global__ void __launch_bounds__(kStreamThreads) add_rmsnorm_stream_kernel(cons
     ss = lane < warps ? red[it & 1][0][lane] : 0.f;
     am = lane < warps ? red[it & 1][1][lane] : 0.f;
     warp_reduce(ss, am);
-    const float inv = 1.f / sqrtf(ss / (float)p.M + p.eps);
+    const float inv = rsqrtf(ss * p.inv_m + p.eps);
     const int k = scale_exponent(am * inv);
     const float up = f8::pow2(-k);
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int c = tid + i * nthr;
-      if (c < at.count) {
-#pragma unroll
-        for (int e = 0; e < VE; ++e) v[i][e] *= inv;
-        const int first = at.first(c), last = at.last(c, p.M);
-        if (p.y) store_granule<T>(p.y, at.g0 + c, v[i], first, last);
-        if (p.codes) store_codes<VE>(p.codes, at.g0 + c, v[i], up, first, last);
-      }
+      if (c < count) second_step<T, false>(p, at, c, v[i], inv, up);
     }
     if (p.codes && tid == 0) p.scales[row] = (uint8_t)(k + 127);
     if (++s == kStages) {
@@ -434,7 +435,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_any_kernel(const Params p) {
     am = fmaxf(am, fabsf(g ? s * to_f32<T>(g[c]) : s));
   }
   block_reduce(ss, am, red);
-  const float inv = g ? 1.f / sqrtf(ss / (float)p.M + p.eps) : 1.f;
+  const float inv = g ? rsqrtf(ss * p.inv_m + p.eps) : 1.f;
   const int k = scale_exponent(am * inv);
   const float up = f8::pow2(-k);
   for (int c = threadIdx.x; c < p.M; c += blockDim.x) {

@@ -1251,19 +1251,7 @@ int32_t device_sms() {
   return sms;
 }
 
-template <typename T, int ITEMS, bool SHIFTED>
-mla_status launch_rms_rows(const mla::rms::Params& p, int granules, cudaStream_t st) {
-  if (granules <= 32 * ITEMS) {
-    const unsigned blocks = (unsigned)(((int64_t)p.T + mla::rms::kWarpRows - 1) / mla::rms::kWarpRows);
-    mla::rms::add_rmsnorm_kernel<T, ITEMS, true, SHIFTED><<<blocks, 32 * mla::rms::kWarpRows, 0, st>>>(p);
-  } else {
-    const int threads = ((granules + ITEMS - 1) / ITEMS + 31) / 32 * 32;
-    mla::rms::add_rmsnorm_kernel<T, ITEMS, false, SHIFTED><<<(unsigned)p.T, threads, 0, st>>>(p);
-  }
-  return launch_check("add_rmsnorm");
-}
-
-// Blocks of the streaming kernel that an SM holds (0: none), asked for once per kernel,
+// Blocks of a kernel that an SM holds (0: not known), asked for once per kernel,
 // block size, shared memory and device.
 int blocks_per_sm(const void* kernel, int threads, int64_t smem) {
   struct Known {
@@ -1285,31 +1273,53 @@ int blocks_per_sm(const void* kernel, int threads, int64_t smem) {
   return blocks;
 }
 
+template <typename T, int ITEMS, bool SHIFTED>
+mla_status launch_rms_rows(const mla::rms::Params& p, int granules, cudaStream_t st) {
+  if (granules <= 32 * ITEMS) {
+    const unsigned blocks = (unsigned)(((int64_t)p.T + mla::rms::kWarpRows - 1) / mla::rms::kWarpRows);
+    mla::rms::add_rmsnorm_kernel<T, ITEMS, true, SHIFTED><<<blocks, 32 * mla::rms::kWarpRows, 0, st>>>(p);
+  } else {
+    const int threads = ((granules + ITEMS - 1) / ITEMS + 31) / 32 * 32;
+    mla::rms::add_rmsnorm_kernel<T, ITEMS, false, SHIFTED><<<(unsigned)p.T, threads, 0, st>>>(p);
+  }
+  return launch_check("add_rmsnorm");
+}
+
+// Rows in whole and aligned granules, many of them: the streaming kernel. It takes rows of
+// 2 KiB and more, and wants a few per block: with fewer its ring never fills (T = 512, M = 7168
+// bf16: 8.3 us either way; T = 1024: 10.4 against 12.5 us; T = 1024, M = 1024: 6.3 against
+// 4.3). Sets *done if it ran.
+template <typename T>
+mla_status launch_rms_stream(const mla::rms::Params& p, cudaStream_t st, bool* done) {
+  constexpr int VE = mla::rms::granule<T>(), kItems = 32 / VE, kMaxSmem = 220 * 1024;
+  const int granules = p.M / VE, threads = ((granules + kItems - 1) / kItems + 31) / 32 * 32;
+  const int64_t smem = (int64_t)mla::rms::kStages * granules * 16 * (p.r ? 2 : 1);
+  const int sms = device_sms();
+  *done = false;
+  if (granules < 128 || threads > mla::rms::kStreamThreads || smem > kMaxSmem || p.T < 2 * sms) return MLA_OK;
+  auto kern = mla::rms::add_rmsnorm_stream_kernel<T, kItems>;
+  if (mla_status s = ensure_smem_attr((const void*)kern, kMaxSmem)) return s;
+  const int64_t resident = (int64_t)sms * blocks_per_sm((const void*)kern, threads, smem);
+  if (resident == 0 || 2 * (int64_t)p.T < 5 * resident) return MLA_OK;
+  *done = true;
+  kern<<<(unsigned)resident, threads, (size_t)smem, st>>>(p, g_timeout_ns.load());
+  return launch_check("add_rmsnorm");
+}
+
 template <typename T, bool SHIFTED>
 mla_status launch_rms(const mla::rms::Params& p, cudaStream_t st) {
   constexpr int VE = mla::rms::granule<T>();
-  const int granules = (int)(mla::rms::stream_row_bytes<T>(p.M) / 16) - (SHIFTED ? 0 : 1);
-  // The streaming kernel takes rows of 2 KiB and more, and wants a few rows per block: with
-  // fewer its ring never fills (T = 512, M = 7168 bf16: 8.3 us either way; T = 1024: 10.4
-  // against 12.5 us; T = 1024, M = 1024: 6.3 against 4.3 us, two rows a block).
-  constexpr int kItems = 32 / VE, kMaxSmem = 220 * 1024;
-  const int64_t smem = mla::rms::stream_smem<T>(p.M, p.r != nullptr);
-  const int threads = ((granules + kItems - 1) / kItems + 31) / 32 * 32;
-  if (p.gain && (int64_t)p.M * sizeof(T) >= 2048 && threads <= mla::rms::kStreamThreads && smem <= kMaxSmem) {
-    auto kern = mla::rms::add_rmsnorm_stream_kernel<T, kItems, SHIFTED>;
-    const int sms = device_sms();
-    if (p.T >= 2 * sms) {
-      if (mla_status s = ensure_smem_attr((const void*)kern, kMaxSmem)) return s;
-      const int64_t resident = (int64_t)sms * blocks_per_sm((const void*)kern, threads, smem);
-      if (resident > 0 && 2 * (int64_t)p.T >= 5 * resident) {
-        kern<<<(unsigned)resident, threads, (size_t)smem, st>>>(p, g_timeout_ns.load());
-        return launch_check("add_rmsnorm");
-      }
-    }
+  if constexpr (!SHIFTED) {
+    bool done = false;
+    if (p.gain)
+      if (mla_status s = launch_rms_stream<T>(p, st, &done)) return s;
+    if (done) return ok();
   }
-  // else the fewest elements a thread that 1024 threads allow
-  if (granules <= 8 / VE * 1024) return launch_rms_rows<T, 8 / VE, SHIFTED>(p, granules, st);
-  if (granules <= 16 / VE * 1024) return launch_rms_rows<T, 16 / VE, SHIFTED>(p, granules, st);
+  // the fewest elements a thread that a block's threads allow
+  const int64_t granules = ((int64_t)p.M + (SHIFTED ? 2 * VE - 2 : 0)) / VE;   // touched at the worst shift
+  if (granules <= 8 / VE * 1024) return launch_rms_rows<T, 8 / VE, SHIFTED>(p, (int)granules, st);
+  if (granules <= 16 / VE * 1024) return launch_rms_rows<T, 16 / VE, SHIFTED>(p, (int)granules, st);
+  if (granules <= 32 / VE * mla::rms::kWideThreads) return launch_rms_rows<T, 32 / VE, SHIFTED>(p, (int)granules, st);
   mla::rms::add_rmsnorm_any_kernel<T><<<(unsigned)p.T, 1024, 0, st>>>(p);
   return launch_check("add_rmsnorm");
 }
@@ -1380,6 +1390,7 @@ mla_status add_rmsnorm(const char* what, const void* x, const void* residual, co
   p.scales = static_cast<uint8_t*>(scales);
   p.T = T;
   p.M = M;
+  p.inv_m = (float)(1.0 / M);
   p.eps = eps;
   return dtype == MLA_BF16 ? launch_rms<__nv_bfloat16>(p, as_stream(stream)) : launch_rms<float>(p, as_stream(stream));
 }

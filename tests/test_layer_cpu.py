@@ -160,3 +160,13 @@ def test_a_strided_tensor_is_refused_not_misread():
         with pytest.raises(mla.MlaError) as e:
             fn(**args)
         assert e.value.status == INVALID
+
+
+def test_a_host_tensor_is_refused():
+    x = torch.zeros(4, 64, dtype=torch.bfloat16)
+    for fn, args in ((mla.mla_add_rmsnorm, norm_args(x=x)), (mla.mla_linear, lin_args(W=x)),
+                     (mla.mla_quantize_fp8, dict(rows=x, codes=2 << 20, scales=3 << 20, n=4, width=64, dtype=0,
+                                                 stream=0))):
+        with pytest.raises(mla.MlaError) as e:
+            fn(**args)
+        assert e.value.status == INVALID
