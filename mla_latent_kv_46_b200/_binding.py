@@ -262,45 +262,46 @@ def mla_prefill_attn(ckr, q_nope, q_rope, W_UK, W_UV, cu_seqlens, cu_seqlens_hos
                                  _stream(stream)), "mla_prefill_attn")
 
 
-def _dense(x):
-    """data_ptr of a contiguous CUDA tensor on the current device (None -> NULL, integers are
+def _dense(*tensors):
+    """data_ptr of contiguous CUDA tensors on the current device (None -> NULL, integers are
     raw addresses). The calls take row-major buffers of the device they launch on, so a
     strided view, a host tensor or another device's is refused, not misread."""
-    if x is None or isinstance(x, int):
-        return x
-    if not x.is_contiguous():
-        raise MlaError(MLA_ERR_INVALID, "argument", "tensor is not contiguous")
-    device = x.get_device()
-    if device < 0:
-        raise MlaError(MLA_ERR_INVALID, "argument", "tensor is not on a CUDA device")
-    import torch
-    if device != torch.cuda.current_device():
-        raise MlaError(MLA_ERR_INVALID, "argument", f"tensor is on device {device}, not the current one")
-    return x.data_ptr()
+    out, device = [], None
+    for x in tensors:
+        if x is not None and type(x) is not int:
+            if not x.is_contiguous():
+                raise MlaError(MLA_ERR_INVALID, "argument", "tensor is not contiguous")
+            d = x.get_device()
+            if d != device:
+                if d < 0:
+                    raise MlaError(MLA_ERR_INVALID, "argument", "tensor is not on a CUDA device")
+                import torch
+                if d != torch.cuda.current_device():
+                    raise MlaError(MLA_ERR_INVALID, "argument", f"tensor is on device {d}, not the current one")
+                device = d
+            x = x.data_ptr()
+        out.append(x)
+    return out
 
 
 def mla_add_rmsnorm(x, residual, gain, residual_out, out, T, M, eps, dtype, stream=None):
-    _check(_lib.mla_add_rmsnorm(_dense(x), _dense(residual), _dense(gain), _dense(residual_out), _dense(out), T, M,
-                                eps, dtype, _stream(stream)), "mla_add_rmsnorm")
+    _check(_lib.mla_add_rmsnorm(*_dense(x, residual, gain, residual_out, out), T, M, eps, dtype, _stream(stream)),
+           "mla_add_rmsnorm")
 
 
 def mla_add_rmsnorm_fp8(x, residual, gain, residual_out, out, codes, scales, T, M, eps, dtype, stream=None):
-    _check(_lib.mla_add_rmsnorm_fp8(_dense(x), _dense(residual), _dense(gain), _dense(residual_out), _dense(out),
-                                    _dense(codes), _dense(scales), T, M, eps, dtype, _stream(stream)),
-           "mla_add_rmsnorm_fp8")
+    _check(_lib.mla_add_rmsnorm_fp8(*_dense(x, residual, gain, residual_out, out, codes, scales), T, M, eps, dtype,
+                                    _stream(stream)), "mla_add_rmsnorm_fp8")
 
 
 def mla_quantize_fp8(rows, codes, scales, n, width, dtype, stream=None):
-    _check(_lib.mla_quantize_fp8(_dense(rows), _dense(codes), _dense(scales), n, width, dtype, _stream(stream)),
-           "mla_quantize_fp8")
+    _check(_lib.mla_quantize_fp8(*_dense(rows, codes, scales), n, width, dtype, _stream(stream)), "mla_quantize_fp8")
 
 
 def mla_linear(x, W, bias, mul, residual, out, T, N, K, act, stream=None):
-    _check(_lib.mla_linear(_dense(x), _dense(W), _dense(bias), _dense(mul), _dense(residual), _dense(out), T, N, K,
-                           act, _stream(stream)), "mla_linear")
+    _check(_lib.mla_linear(*_dense(x, W, bias, mul, residual, out), T, N, K, act, _stream(stream)), "mla_linear")
 
 
 def mla_linear_fp8(x_codes, x_scales, W_codes, W_scales, bias, mul, residual, out, T, N, K, act, stream=None):
-    _check(_lib.mla_linear_fp8(_dense(x_codes), _dense(x_scales), _dense(W_codes), _dense(W_scales), _dense(bias),
-                               _dense(mul), _dense(residual), _dense(out), T, N, K, act, _stream(stream)),
-           "mla_linear_fp8")
+    _check(_lib.mla_linear_fp8(*_dense(x_codes, x_scales, W_codes, W_scales, bias, mul, residual, out), T, N, K, act,
+                               _stream(stream)), "mla_linear_fp8")

@@ -24,16 +24,21 @@ struct Params {
   const uint8_t* xs;           // [T] scale bytes (8-bit operands)
   const uint8_t* ws;           // [N]
   int32_t T, N, K, act;
+  bool quads;                  // four neighbouring features can be moved in one access
+  int32_t nt, stages;          // tensor-core kernels: tokens per tile, stages of the ring
   uint64_t timeout_ns;
 };
 
 // 2^(byte - 127); the bytes the quantisers write are 1 .. 134.
 __device__ __forceinline__ float scale_of(uint8_t b) { return __uint_as_float((uint32_t)b << 23); }
 
+// exp by ex2.approx and the quotient by rcp.approx, a few units in 2^-22 off (the result is
+// rounded to bf16, 2^-9): a full division took a third of the epilogue's instructions. Sums so
+// negative that e^-v overflows give 0, as the formulas do.
 __device__ __forceinline__ float activate(float v, int act) {
   switch (act) {
-    case kActSigmoid: return 1.f / (1.f + __expf(-v));
-    case kActSilu: return v / (1.f + __expf(-v));
+    case kActSigmoid: return __fdividef(1.f, 1.f + __expf(-v));
+    case kActSilu: return __fdividef(v, 1.f + __expf(-v));
     case kActGelu: return 0.5f * v * erfcf(-0.70710678118654752f * v);
     default: return v;
   }

@@ -1409,58 +1409,79 @@ mla_status linear_maps(CUtensorMap* tw, CUtensorMap* tx, const void* W, const vo
   return make_map_2d(tx, x, K, (uint64_t)p.T, K * 2, x_rows);
 }
 
-template <bool F8, int NT, int STAGES>
-mla_status launch_linear_split(const void* x, const void* W, const mla::lin::Params& p, int32_t sms, cudaStream_t st,
-                               const char* what) {
-  using C = mla::lin::SplitCfg<F8, NT, STAGES>;
-  auto kern = mla::lin::linear_split_kernel<F8, NT, STAGES>;
-  CUtensorMap tw, tx;
-  if (mla_status s = linear_maps<F8>(&tw, &tx, W, x, p, mla::lin::kM, NT)) return s;
-  if (mla_status s = ensure_smem_attr((const void*)kern, C::kSmemBytes)) return s;
-  const int64_t tiles_n = ((int64_t)p.N + mla::lin::kM - 1) / mla::lin::kM, tiles_t = ((int64_t)p.T + NT - 1) / NT;
-  const int kblk = (p.K + mla::lin::kb_elems<F8>() - 1) / mla::lin::kb_elems<F8>();
-  // K slices: as many CTAs as the GPU holds at once (two per SM where shared memory allows)
-  const int64_t room = (int64_t)sms * (C::kSmemBytes <= 113 * 1024 ? 2 : 1);
-  const int slices = (int)std::max<int64_t>(1, std::min<int64_t>({room / (tiles_n * tiles_t), 8, (kblk + 1) / 2}));
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)slices, (unsigned)tiles_n, (unsigned)tiles_t);
-  cfg.blockDim = dim3(128);
-  cfg.dynamicSmemBytes = C::kSmemBytes;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)slices;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  MLA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, tw, tx, p));
-  return launch_check(what);
-}
+// Shared memory a block may have where an SM is to hold two (each takes 1 KiB more), or one.
+constexpr int kSmemOfTwo = 113 * 1024, kSmemOfOne = 226 * 1024;
 
-template <bool F8, int NT, int STAGES>
-mla_status launch_linear_pair(const void* x, const void* W, const mla::lin::Params& p, int32_t sms, cudaStream_t st,
-                              const char* what) {
-  using C = mla::lin::PairCfg<F8, NT, STAGES>;
-  auto kern = mla::lin::linear_pair_kernel<F8, NT, STAGES>;
-  CUtensorMap tw, tx;
-  if (mla_status s = linear_maps<F8>(&tw, &tx, W, x, p, mla::lin::kM, NT / 2)) return s;
-  if (mla_status s = ensure_smem_attr((const void*)kern, C::kSmemBytes)) return s;
-  const int64_t tiles = (((int64_t)p.N + 2 * mla::lin::kM - 1) / (2 * mla::lin::kM)) * (((int64_t)p.T + NT - 1) / NT);
-  const unsigned pairs = (unsigned)std::min<int64_t>(tiles, std::max(1, sms / 2));
-  kern<<<2 * pairs, C::kThreads, C::kSmemBytes, st>>>(tw, tx, p);
+// Launches with the programmatic attribute: the kernel's set-up may run under the tail of the
+// kernel before it on the stream (it waits for that one before it touches global memory).
+template <class Kernel, class... Args>
+mla_status launch_overlapped(const char* what, Kernel kern, dim3 grid, int threads, int smem, int cluster,
+                             cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  MLA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, args...));
   return launch_check(what);
 }
 
 template <bool F8>
+mla_status launch_linear_split(const void* x, const void* W, mla::lin::Params p, int nt, int slices, int32_t sms,
+                               cudaStream_t st, const char* what) {
+  using namespace mla::lin;
+  auto kern = linear_split_kernel<F8>;
+  CUtensorMap tw, tx;
+  if (mla_status s = linear_maps<F8>(&tw, &tx, W, x, p, kM, (uint32_t)nt / 2)) return s;
+  if (mla_status s = ensure_smem_attr((const void*)kern, kSmemOfOne)) return s;
+  const int64_t tiles_n = ((int64_t)p.N + 2 * kM - 1) / (2 * kM), tiles_t = ((int64_t)p.T + nt - 1) / nt;
+  // two CTAs an SM where there are that many and they fit; else one, with all of its memory
+  const bool two = 2 * slices * tiles_n * tiles_t > sms && split_smem(nt, 2, slices) <= kSmemOfTwo;
+  p.nt = nt;
+  p.stages = std::min(kMaxStages, ((two ? kSmemOfTwo : kSmemOfOne) - kSmemSlack) / stage_bytes_of(nt));
+  return launch_overlapped(what, kern, dim3(2 * (unsigned)slices, (unsigned)tiles_n, (unsigned)tiles_t), kSplitThreads,
+                           split_smem(nt, p.stages, slices), 2 * slices, st, tw, tx, p);
+}
+
+template <bool F8>
+mla_status launch_linear_pair(const void* x, const void* W, mla::lin::Params p, int nt, int32_t sms, cudaStream_t st,
+                              const char* what) {
+  using namespace mla::lin;
+  auto kern = linear_pair_kernel<F8>;
+  CUtensorMap tw, tx;
+  if (mla_status s = linear_maps<F8>(&tw, &tx, W, x, p, kM, (uint32_t)nt / 2)) return s;
+  if (mla_status s = ensure_smem_attr((const void*)kern, kSmemOfOne)) return s;
+  p.nt = nt;
+  p.stages = std::min(kMaxStages, (kSmemOfOne - kSmemSlack) / stage_bytes_of(nt));
+  const int64_t tiles = (((int64_t)p.N + 2 * kM - 1) / (2 * kM)) * (((int64_t)p.T + nt - 1) / nt);
+  const unsigned pairs = (unsigned)std::min<int64_t>(tiles, std::max(1, sms / 2));
+  return launch_overlapped(what, kern, dim3(2 * pairs), kPairThreads, pair_smem(nt, p.stages), 0, st, tw, tx, p);
+}
+
+template <bool F8>
 mla_status linear_tc(const void* x, const void* W, const mla::lin::Params& p, cudaStream_t st, const char* what) {
+  using namespace mla::lin;
   const int32_t sms = device_sms();
-  if (p.T <= 16) return launch_linear_split<F8, 16, 6>(x, W, p, sms, st, what);
-  if (p.T <= 32) return launch_linear_split<F8, 32, 5>(x, W, p, sms, st, what);
-  if (p.T <= 64) return launch_linear_split<F8, 64, 4>(x, W, p, sms, st, what);
-  if (p.T <= 128) return launch_linear_split<F8, 128, 3>(x, W, p, sms, st, what);
-  if (p.T <= 256) return launch_linear_split<F8, 256, 4>(x, W, p, sms, st, what);
-  return launch_linear_pair<F8, 256, 6>(x, W, p, sms, st, what);
+  if (p.T <= 256) {
+    const int nt = (p.T + 15) / 16 * 16;
+    const int64_t tiles = ((int64_t)p.N + 2 * kM - 1) / (2 * kM);
+    const int kblk = (p.K + kb_elems<F8>() - 1) / kb_elems<F8>();
+    // K slices: as many CTAs as the GPU holds at once (two per SM where shared memory allows)
+    const int64_t room = (int64_t)sms * (split_smem(nt, 2, kMaxSlices) <= kSmemOfTwo ? 2 : 1) / 2;
+    int slices = 1;
+    while (2 * slices <= kMaxSlices && 2 * slices * tiles <= room && 4 * slices <= kblk) slices *= 2;
+    return launch_linear_split<F8>(x, W, p, nt, slices, sms, st, what);
+  }
+  return launch_linear_pair<F8>(x, W, p, 256, sms, st, what);
 }
 
 mla_status linear(const char* what, bool f8, const void* x, const void* xs, const void* W, const void* ws,
@@ -1490,6 +1511,9 @@ mla_status linear(const char* what, bool f8, const void* x, const void* xs, cons
   p.N = N;
   p.K = K;
   p.act = act;
+  p.quads = N % 4 == 0;
+  for (const void* q : {bias, mul, residual, (const void*)out})
+    p.quads = p.quads && reinterpret_cast<uintptr_t>(q) % 8 == 0;
   p.timeout_ns = g_timeout_ns.load();
   cudaStream_t st = as_stream(stream);
   // what TMA needs: 16-byte aligned operands and rows; the token and feature tile numbers

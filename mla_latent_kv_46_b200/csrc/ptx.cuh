@@ -118,6 +118,14 @@ __device__ __forceinline__ void prefetch_tmap(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
+// Programmatic dependent launch. A kernel launched with the programmatic attribute may start
+// while the kernel before it on the stream still runs: grid_wait blocks until that one has
+// completed and its writes are visible, and comes before the first access to global memory.
+// grid_launch_next lets the next such kernel's blocks be placed once every block of this one
+// has called it (or exited); the next kernel's own grid_wait still waits for all of this one.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Shared-memory writes by threads (generic proxy) made visible to the tensor
 // core / TMA (async proxy).
 __device__ __forceinline__ void fence_proxy_async_smem() {
