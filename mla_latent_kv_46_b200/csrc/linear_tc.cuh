@@ -90,20 +90,25 @@ __device__ __forceinline__ void unpack4(const uint2& w, float (&f)[4]) {
 
 // The epilogue of `items` quads (features n .. n + 3 of one token; the thread's n is the same
 // for all of its items), items tid, tid + threads, ..: token(i) is item i's token, sums(i, v)
-// its fp32 sums. kQuadBatch items at a time: their mul and residual are all loaded before the
+// its fp32 sums, c the constants of the features. kQuadBatch items at a time: their mul and residual are all loaded before the
 // first is used (out may be either's buffer, so the compiler may not move a load above an
 // earlier item's store).
 constexpr int kQuadBatch = 4;
+template <bool F8>
+struct QuadConstants {
+  float bias[4], ws[4];
+  __device__ __forceinline__ QuadConstants(const Params& p, int32_t n) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      bias[j] = p.bias && n + j < p.N ? __bfloat162float(p.bias[n + j]) : 0.f;
+      ws[j] = F8 && n + j < p.N ? scale_of(p.ws[n + j]) : 1.f;
+    }
+  }
+};
 template <bool F8, class Token, class Sums>
 __device__ __forceinline__ void finish_quads(const Params& p, int items, int tid, int threads, int32_t n,
-                                             const Token& token, const Sums& sums) {
+                                             const QuadConstants<F8>& c, const Token& token, const Sums& sums) {
   if (n >= p.N) return;
-  float bias[4], ws[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    bias[j] = p.bias && n + j < p.N ? __bfloat162float(p.bias[n + j]) : 0.f;
-    ws[j] = F8 && n + j < p.N ? scale_of(p.ws[n + j]) : 1.f;
-  }
   for (int i0 = tid; i0 < items; i0 += kQuadBatch * threads) {
     int64_t at[kQuadBatch];
     uint2 m[kQuadBatch], r[kQuadBatch];
@@ -126,7 +131,7 @@ __device__ __forceinline__ void finish_quads(const Params& p, int items, int tid
       float v[4];
       sums(i, v);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = activate((F8 ? v[j] * ws[j] * xs[b] : v[j]) + bias[j], p.act);
+      for (int j = 0; j < 4; ++j) v[j] = activate((F8 ? v[j] * c.ws[j] * xs[b] : v[j]) + c.bias[j], p.act);
       if (p.quads) {
         float f[4];
         if (p.mul) {
@@ -155,6 +160,8 @@ __device__ __forceinline__ void finish_quads(const Params& p, int items, int tid
   }
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* q) { asm volatile("prefetch.global.L2 [%0];" ::"l"(q)); }
+
 // Asks L2 for `count` rows of `width` elements of mul and residual, from row t0 and column n0
 // on (32 lanes of a warp; `w` of `warps` warps): they come from HBM under the main loop.
 __device__ __forceinline__ void prefetch_rows(const Params& p, int64_t t0, int count, int32_t n0, int width, int w,
@@ -164,8 +171,8 @@ __device__ __forceinline__ void prefetch_rows(const Params& p, int64_t t0, int c
   const int lines = (cols * 2 + 127) / 128 + 1;      // 128-byte lines a row may touch
   for (int i = w * 32 + lane; i < count * lines; i += warps * 32) {
     const int64_t at = (t0 + i / lines) * p.N + n0 + min(64 * (i % lines), cols - 1);
-    if (p.mul) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.mul + at));
-    if (p.res) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.res + at));
+    if (p.mul) prefetch_l2(p.mul + at);
+    if (p.res) prefetch_l2(p.res + at);
   }
 }
 
@@ -267,6 +274,9 @@ __global__ void __launch_bounds__(kSplitThreads) linear_split_kernel(const __gri
     // ---------------------------------------------------------------- loads
     const bool leader = ptx::elect_one();
     const int32_t trow = (int32_t)t0 + nt / 2 * (int)r;
+    // with one token tile W is read once and by this pair alone: it should not push the
+    // epilogue's operands, fetched early, out of L2
+    const uint64_t w_policy = gridDim.z == 1 ? ptx::policy_evict_first() : ptx::policy_evict_normal();
     int s = 0, issued = 0;
     uint32_t parity = 1;
     for (int i = 0; i < nkb; ++i) {
@@ -274,7 +284,7 @@ __global__ void __launch_bounds__(kSplitThreads) linear_split_kernel(const __gri
       if (leader) {
         const uint32_t sa = sbase + s * stage_bytes, sb = sa + kABytes;
         if (even) ptx::mbar_arrive_expect_tx(bar(kFull + s), 2 * stage_bytes);
-        ptx::tma_load_2d_pair(sa, &tmW, lead(bar(kFull + s)), (kb0 + i) * kb_elems<F8>(), n0);
+        ptx::tma_load_2d_pair_hint(sa, &tmW, lead(bar(kFull + s)), (kb0 + i) * kb_elems<F8>(), n0, w_policy);
         ptx::tma_load_2d_pair(sb, &tmX, lead(bar(kFull + s)), (kb0 + i) * kb_elems<F8>(), trow);
       }
       issued = i + 1;
@@ -320,6 +330,9 @@ __global__ void __launch_bounds__(kSplitThreads) linear_split_kernel(const __gri
   const int tokens = (int)min((int64_t)nt, p.T - t0);
   if (warp >= 3 && (p.mul || p.res) && slice == 0)
     prefetch_rows(p, t0, tokens, n0, kM, warp - 3, kSplitThreads / 32 - 3, lane);
+  if (F8 && warp == 2 && lane <= tokens / 128) prefetch_l2(p.xs + t0 + min(128 * lane, tokens - 1));
+  const int32_t n = n0 + 4 * (tid % (kM / 4));
+  const QuadConstants<F8> constants(p, n);
   const bool done = ok && wait_all(bar(kDone), 0);
   if (!done) give_up();
   ptx::tc_fence_after();
@@ -358,7 +371,7 @@ __global__ void __launch_bounds__(kSplitThreads) linear_split_kernel(const __gri
     const bool has_last = (chunks - 1) % slices == slice;
     const int items = mine * kItems - (has_last ? (chunks * kChunk - tokens) * kQuads : 0);
     finish_quads<F8>(
-        p, items, tid, kSplitThreads, n0 + 4 * (tid % kQuads),
+        p, items, tid, kSplitThreads, n, constants,
         [&](int i) { return t0 + (int64_t)(i / kItems * slices + slice) * kChunk + i % kItems / kQuads; },
         [&](int i, float (&v)[4]) {
           v[0] = v[1] = v[2] = v[3] = 0.f;
