@@ -24,7 +24,7 @@ struct Params {
   const uint8_t* xs;           // [T] scale bytes (8-bit operands)
   const uint8_t* ws;           // [N]
   int32_t T, N, K, act;
-  bool quads;                  // four neighbouring features can be moved in one access
+  bool octs;                   // eight neighbouring features can be moved in one access
   int32_t nt, stages;          // tensor-core kernels: tokens per tile, stages of the ring
   uint64_t timeout_ns;
 };

@@ -30,7 +30,7 @@ namespace lin {
 constexpr int kM = 128;              // features (MMA rows) per CTA
 constexpr int kKBytes = 128;         // bytes of a K block of one row
 constexpr int kABytes = kM * kKBytes;
-constexpr int kMaxSlices = 4;        // pairs of CTAs of a portable cluster
+constexpr int kMaxSlices = 8;        // pairs of CTAs of the largest cluster
 
 template <bool F8> __host__ __device__ constexpr int kb_elems() { return F8 ? 128 : 64; }
 
@@ -81,83 +81,53 @@ __device__ __forceinline__ void finish_tokens(const Params& p, float (&v)[CNT], 
     if (j < tokens) p.out[at + (int64_t)j * p.N] = __float2bfloat16_rn(v[j]);
 }
 
-__device__ __forceinline__ void unpack4(const uint2& w, float (&f)[4]) {
-  f[0] = __uint_as_float(w.x << 16);
-  f[1] = __uint_as_float(w.x & 0xFFFF0000u);
-  f[2] = __uint_as_float(w.y << 16);
-  f[3] = __uint_as_float(w.y & 0xFFFF0000u);
-}
-
-// The epilogue of `items` quads (features n .. n + 3 of one token; the thread's n is the same
-// for all of its items), items tid, tid + threads, ..: token(i) is item i's token, sums(i, v)
-// its fp32 sums, c the constants of the features. kQuadBatch items at a time: their mul and residual are all loaded before the
-// first is used (out may be either's buffer, so the compiler may not move a load above an
-// earlier item's store).
-constexpr int kQuadBatch = 4;
+// Where N and every pointer allow it (p.octs), the epilogue moves eight neighbouring features
+// of one token at a time, 16 bytes: one thread's mul, residual and out are one access each,
+// and cost a fifth of the instructions of single elements.
 template <bool F8>
-struct QuadConstants {
-  float bias[4], ws[4];
-  __device__ __forceinline__ QuadConstants(const Params& p, int32_t n) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      bias[j] = p.bias && n + j < p.N ? __bfloat162float(p.bias[n + j]) : 0.f;
-      ws[j] = F8 && n + j < p.N ? scale_of(p.ws[n + j]) : 1.f;
-    }
+struct OctConstants {   // as they lie in memory: unpacked where they are used
+  uint4 bias;
+  uint2 ws;
+  __device__ __forceinline__ void load(const Params& p, int32_t n) {
+    bias = make_uint4(0, 0, 0, 0);
+    if (p.bias && n < p.N) bias = *reinterpret_cast<const uint4*>(p.bias + n);
+    if (F8 && n < p.N) ws = *reinterpret_cast<const uint2*>(p.ws + n);
   }
 };
-template <bool F8, class Token, class Sums>
-__device__ __forceinline__ void finish_quads(const Params& p, int items, int tid, int threads, int32_t n,
-                                             const QuadConstants<F8>& c, const Token& token, const Sums& sums) {
-  if (n >= p.N) return;
-  for (int i0 = tid; i0 < items; i0 += kQuadBatch * threads) {
-    int64_t at[kQuadBatch];
-    uint2 m[kQuadBatch], r[kQuadBatch];
-    float xs[kQuadBatch];
+template <bool F8>
+__device__ __forceinline__ void finish_oct(const Params& p, float (&v)[8], const uint4& mul, const uint4& res, float xs,
+                                           const OctConstants<F8>& c, int64_t at) {
+  float f[8];
+  if (F8) {
 #pragma unroll
-    for (int b = 0; b < kQuadBatch; ++b) {
-      const int i = i0 + b * threads;
-      if (i < items) {
-        const int64_t t = token(i);
-        at[b] = t * p.N + n;
-        if (F8) xs[b] = scale_of(p.xs[t]);
-        if (p.quads && p.mul) m[b] = *reinterpret_cast<const uint2*>(p.mul + at[b]);
-        if (p.quads && p.res) r[b] = *reinterpret_cast<const uint2*>(p.res + at[b]);
-      }
-    }
-#pragma unroll
-    for (int b = 0; b < kQuadBatch; ++b) {
-      const int i = i0 + b * threads;
-      if (i >= items) break;
-      float v[4];
-      sums(i, v);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = activate((F8 ? v[j] * c.ws[j] * xs[b] : v[j]) + c.bias[j], p.act);
-      if (p.quads) {
-        float f[4];
-        if (p.mul) {
-          unpack4(m[b], f);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] *= f[j];
-        }
-        if (p.res) {
-          unpack4(r[b], f);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v[j] += f[j];
-        }
-        const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
-        *reinterpret_cast<uint2*>(p.out + at[b]) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (n + j < p.N) {
-            if (p.mul) v[j] *= __bfloat162float(p.mul[at[b] + j]);
-            if (p.res) v[j] += __bfloat162float(p.res[at[b] + j]);
-            p.out[at[b] + j] = __float2bfloat16_rn(v[j]);
-          }
-      }
-    }
+    for (int j = 0; j < 8; ++j) v[j] = v[j] * scale_of((uint8_t)((j < 4 ? c.ws.x : c.ws.y) >> (8 * (j % 4)))) * xs;
   }
+  if (p.bias) {
+    f8::unpack8(c.bias, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += f[j];
+  }
+  if (p.act != kActNone) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = activate(v[j], p.act);
+  }
+  if (p.mul) {
+    f8::unpack8(mul, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] *= f[j];
+  }
+  if (p.res) {
+    f8::unpack8(res, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] += f[j];
+  }
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+    o[j] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p.out + at) = make_uint4(o[0], o[1], o[2], o[3]);
 }
 
 __device__ __forceinline__ void prefetch_l2(const void* q) { asm volatile("prefetch.global.L2 [%0];" ::"l"(q)); }
@@ -331,8 +301,17 @@ __global__ void __launch_bounds__(kSplitThreads) linear_split_kernel(const __gri
   if (warp >= 3 && (p.mul || p.res) && slice == 0)
     prefetch_rows(p, t0, tokens, n0, kM, warp - 3, kSplitThreads / 32 - 3, lane);
   if (F8 && warp == 2 && lane <= tokens / 128) prefetch_l2(p.xs + t0 + min(128 * lane, tokens - 1));
-  const int32_t n = n0 + 4 * (tid % (kM / 4));
-  const QuadConstants<F8> constants(p, n);
+  // this thread's features in the last step: eight, or one
+  constexpr int kOcts = kM / 8;
+  const int32_t n = p.octs ? n0 + 8 * (tid % kOcts) : n0 + tid % kM;
+  OctConstants<F8> constants;
+  float bias = 0.f, ws = 1.f;
+  if (p.octs) {
+    constants.load(p, n);
+  } else if (n < p.N) {
+    if (p.bias) bias = __bfloat162float(p.bias[n]);
+    if (F8) ws = scale_of(p.ws[n]);
+  }
   const bool done = ok && wait_all(bar(kDone), 0);
   if (!done) give_up();
   ptx::tc_fence_after();
@@ -362,29 +341,82 @@ __global__ void __launch_bounds__(kSplitThreads) linear_split_kernel(const __gri
   }
   __syncthreads();
   if (slices > 1) ptx::cluster_sync();   // every slice's sums are here; nothing remote is touched from now on
-  if (done && slice < chunks) {
-    // four neighbouring features of a token per thread, added in slice order
-    const float4* part = reinterpret_cast<const float4*>(smem);
-    constexpr int kQuads = kM / 4, kItems = kChunk * kQuads;
-    // this CTA's tokens: whole chunks, but for the last of all
+  if (done && slice < chunks && n < p.N) {
+    // the slices' sums added in their order, for this CTA's tokens: whole chunks, but for the
+    // last of all
+    const float* part = reinterpret_cast<const float*>(smem);
+    const int stride = per * kChunk * kM;       // from one slice's sums to the next's
     const int mine = (chunks - slice + slices - 1) / slices;
-    const bool has_last = (chunks - 1) % slices == slice;
-    const int items = mine * kItems - (has_last ? (chunks * kChunk - tokens) * kQuads : 0);
-    finish_quads<F8>(
-        p, items, tid, kSplitThreads, n, constants,
-        [&](int i) { return t0 + (int64_t)(i / kItems * slices + slice) * kChunk + i % kItems / kQuads; },
-        [&](int i, float (&v)[4]) {
-          v[0] = v[1] = v[2] = v[3] = 0.f;
+    const int held = mine * kChunk - ((chunks - 1) % slices == slice ? chunks * kChunk - tokens : 0);
+    auto token_of = [&](int i) { return t0 + (int64_t)(i / kChunk * slices + slice) * kChunk + i % kChunk; };
+    constexpr int kBatch = 4;   // tokens whose operands are loaded before the first is finished: out may
+                                // be mul's or residual's buffer, so no load moves above an earlier store
+    if (p.octs) {
+      constexpr int kStep = kSplitThreads / kOcts;
+      for (int i0 = tid / kOcts; i0 < held; i0 += kBatch * kStep) {
+        uint4 m[kBatch], r[kBatch];
+        float xs[kBatch];
 #pragma unroll
-          for (int s = 0; s < kMaxSlices; ++s)
-            if (s < slices) {
-              const float4 w = part[s * per * kItems + i];
-              v[0] += w.x;
-              v[1] += w.y;
-              v[2] += w.z;
-              v[3] += w.w;
-            }
-        });
+        for (int b = 0; b < kBatch; ++b) {
+          const int i = i0 + b * kStep;
+          if (i < held) {
+            const int64_t t = token_of(i), at = t * p.N + n;
+            if (F8) xs[b] = scale_of(p.xs[t]);
+            if (p.mul) m[b] = *reinterpret_cast<const uint4*>(p.mul + at);
+            if (p.res) r[b] = *reinterpret_cast<const uint4*>(p.res + at);
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const int i = i0 + b * kStep;
+          if (i < held) {
+            float v[8] = {};
+#pragma unroll
+            for (int s = 0; s < kMaxSlices; ++s)
+              if (s < slices) {
+                const float4* w = reinterpret_cast<const float4*>(part + s * stride + i * kM + 8 * (tid % kOcts));
+                const float4 lo = w[0], hi = w[1];
+                v[0] += lo.x;
+                v[1] += lo.y;
+                v[2] += lo.z;
+                v[3] += lo.w;
+                v[4] += hi.x;
+                v[5] += hi.y;
+                v[6] += hi.z;
+                v[7] += hi.w;
+              }
+            finish_oct<F8>(p, v, m[b], r[b], xs[b], constants, token_of(i) * p.N + n);
+          }
+        }
+      }
+    } else {
+      constexpr int kStep = kSplitThreads / kM;
+      for (int i0 = tid / kM; i0 < held; i0 += kBatch * kStep) {
+        float v[kBatch], m[kBatch], r[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const int i = i0 + b * kStep;
+          if (i < held) {
+            const int64_t t = token_of(i), at = t * p.N + n;
+            v[b] = 0.f;
+            for (int s = 0; s < slices; ++s) v[b] += part[s * stride + i * kM + tid % kM];
+            if (F8) v[b] = v[b] * ws * scale_of(p.xs[t]);
+            if (p.mul) m[b] = __bfloat162float(p.mul[at]);
+            if (p.res) r[b] = __bfloat162float(p.res[at]);
+          }
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const int i = i0 + b * kStep;
+          if (i < held) {
+            float y = activate(v[b] + bias, p.act);
+            if (p.mul) y *= m[b];
+            if (p.res) y += r[b];
+            p.out[token_of(i) * p.N + n] = __float2bfloat16_rn(y);
+          }
+        }
+      }
+    }
   }
   ptx::tc_fence_before();
   __syncthreads();
@@ -398,28 +430,45 @@ __global__ void __launch_bounds__(kSplitThreads) linear_split_kernel(const __gri
 
 // ------------------------------------------------------------------ many tokens: SM pairs
 // p.nt tokens a tile (a multiple of 16, at most 256; two accumulators in TMEM), p.stages
-// stages. Warp 0 loads, warp 1 issues the MMAs (even CTA), warps 2 and 3 fetch the epilogue's
-// operands into L2, warps 4.. run the epilogue (two per 32 TMEM lanes, on alternate chunks).
-constexpr int kEpiWarps = 8;
+// stages. Warp 0 loads, warp 1 issues the MMAs (even CTA), warps 4.. run the epilogue (two per
+// 32 TMEM lanes, on alternate chunks of 16 tokens); with p.octs they bring mul and residual
+// into shared memory by TMA, kOpSlots chunks ahead, else warps 2 and 3 fetch them into L2.
+// (Loaded into registers one chunk ahead instead, the operands of a 4096 x 7168 output kept
+// ~8 KiB in flight per SM and took 29 us.)
+constexpr int kEpiWarps = 8, kEpiSets = kEpiWarps / 4;
 constexpr int kPairThreads = 32 * (4 + kEpiWarps);
-__host__ __device__ constexpr int pair_smem(int nt, int stages) { return stages * stage_bytes_of(nt) + kSmemSlack; }
+constexpr int kOpSlots = 3;
+constexpr int kOpBytes = kChunk * 32 * 2;      // one operand of a warp's chunk: 16 tokens x 32 features
+// behind the ring: per epilogue warp, 16 tokens x 32 features of sums, on their way from the
+// lanes that own a feature to the lanes that own eight (rows of 36 words: no bank conflicts),
+// and its operand slots
+constexpr int kTurnPitch = 36, kTurnBytes = kChunk * kTurnPitch * 4;
+constexpr int kPairBarBytes = 512, kPairSlack = kPairBarBytes + 1024;
+static_assert(8 * (2 * kMaxStages + 4 + kEpiWarps * kOpSlots) + 16 <= kPairBarBytes, "barriers");
+__host__ __device__ constexpr int pair_extra(int ops) { return kEpiWarps * (kTurnBytes + ops * kOpSlots * kOpBytes); }
+__host__ __device__ constexpr int pair_smem(int nt, int stages, int ops) {
+  return stages * stage_bytes_of(nt) + pair_extra(ops) + kPairSlack;
+}
 
 constexpr int kGroupT = 8;   // token tiles that share a sweep over the feature tiles
 
 // Tile `i` of tiles_n x tiles_t: groups of kGroupT token tiles, within a group the token
 // tile fastest, so the pairs at work at one time share feature and token tiles in L2.
-__device__ __forceinline__ void tile_of(int64_t i, int tiles_n, int tiles_t, int& tn, int& tt) {
-  const int64_t per = (int64_t)kGroupT * tiles_n;
-  const int g = (int)(i / per);
-  const int first = g * kGroupT, width = min(kGroupT, tiles_t - first);
-  const int64_t rem = i - (int64_t)g * per;
-  tn = (int)(rem / width);
-  tt = first + (int)(rem % width);
+// (32-bit division: 64-bit ones took a microsecond a tile.)
+struct TileAt {
+  int tn, tt;
+};
+__device__ __forceinline__ TileAt tile_of(uint32_t i, uint32_t tiles_n, uint32_t tiles_t) {
+  const uint32_t per = kGroupT * tiles_n, g = i / per, rem = i - g * per;
+  const uint32_t first = g * kGroupT, width = min((uint32_t)kGroupT, tiles_t - first);
+  return TileAt{(int)(rem / width), (int)(first + rem % width)};
 }
 
 template <bool F8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
-linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Params p) {
+linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                   const __grid_constant__ CUtensorMap tmMul, const __grid_constant__ CUtensorMap tmRes,
+                   const Params p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = ptx::smem_u32(smem);
@@ -427,16 +476,19 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
   // CTA), accumulator free (even CTA: both CTAs' epilogue warps)
   const int nt = p.nt, stages = p.stages;
   const uint32_t stage_bytes = (uint32_t)stage_bytes_of(nt);
-  const int off_bar = stages * (int)stage_bytes, kOffMisc = off_bar + 8 * (2 * stages + 4);
+  const int ops = p.octs ? (p.mul != nullptr) + (p.res != nullptr) : 0;
+  const int off_ops = stages * (int)stage_bytes, off_turn = off_ops + kEpiWarps * ops * kOpSlots * kOpBytes;
+  const int off_bar = stages * (int)stage_bytes + pair_extra(ops);
   auto bar = [&](int i) { return sbase + off_bar + 8u * i; };
   const int kFull = 0, kEmpty = stages, kAccFull = 2 * stages, kAccFree = 2 * stages + 2;
+  const int kOps = 2 * stages + 4, kOffMisc = off_bar + 8 * (2 * stages + 4 + kEpiWarps * kOpSlots);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 8);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = ptx::cluster_rank();
   const bool even = rank == 0;
   auto lead = [&](uint32_t a) { return ptx::map_peer(a, 0); };
   const int tiles_n = (p.N + 2 * kM - 1) / (2 * kM), tiles_t = (int)(((int64_t)p.T + nt - 1) / nt);
-  const int64_t tiles = (int64_t)tiles_n * tiles_t;
+  const int tiles = tiles_n * tiles_t;      // below 2^31 - pairs: the host checks
   const int pairs = gridDim.x / 2, pair = blockIdx.x / 2;
   const int kblk = (p.K + kb_elems<F8>() - 1) / kb_elems<F8>();
 
@@ -450,6 +502,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
       ptx::mbar_init(bar(kAccFull + b), 1);
       ptx::mbar_init(bar(kAccFree + b), 2 * kEpiWarps);
     }
+    for (int i = 0; i < kEpiWarps * kOpSlots; ++i) ptx::mbar_init(bar(kOps + i), 1);
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&tmW);
     ptx::prefetch_tmap(&tmX);
@@ -484,10 +537,9 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     int s = 0;
     uint32_t parity = 1;
     bool ok = true;
-    for (int64_t i = pair; i < tiles && ok; i += pairs) {
-      int tn, tt;
-      tile_of(i, tiles_n, tiles_t, tn, tt);
-      const int32_t nrow = tn * 2 * kM + kM * (int)rank, trow = tt * nt + nt / 2 * (int)rank;
+    for (int i = pair; i < tiles && ok; i += pairs) {
+      const TileAt at = tile_of(i, tiles_n, tiles_t);
+      const int32_t nrow = at.tn * 2 * kM + kM * (int)rank, trow = at.tt * nt + nt / 2 * (int)rank;
       for (int kb = 0; kb < kblk; ++kb, ++g) {
         if (!wait_all(bar(kEmpty + s), parity)) { give_up(); ok = false; break; }
         if (leader) {
@@ -515,7 +567,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
       int s = 0, u = 0;  // u: tiles of this pair so far
       uint32_t parity = 0;
       bool ok = true;
-      for (int64_t i = pair; i < tiles && ok; i += pairs, ++u) {
+      for (int i = pair; i < tiles && ok; i += pairs, ++u) {
         const int b = u & 1;
         if (!wait_all(bar(kAccFree + b), (uint32_t)((u >> 1) & 1) ^ 1u)) { give_up(); break; }
         ptx::tc_fence_after();
@@ -544,53 +596,166 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     }
   } else if (warp < 4) {
     // ---------------------------------------------------------------- the epilogue's operands into L2
-    if (p.mul || p.res) {
+    if (!p.octs && (p.mul || p.res)) {
       int u = 0;
-      for (int64_t i = pair; i < tiles; i += pairs, ++u) {
+      for (int i = pair; i < tiles; i += pairs, ++u) {
         // a tile's own main loop is the time to fetch its operands: wait for the one before it
         if (u > 0 && !wait_all(bar(kAccFull + ((u - 1) & 1)), (uint32_t)(((u - 1) >> 1) & 1))) break;
-        int tn, tt;
-        tile_of(i, tiles_n, tiles_t, tn, tt);
-        const int64_t t0 = (int64_t)tt * nt;
-        prefetch_rows(p, t0, (int)min((int64_t)nt, p.T - t0), tn * 2 * kM + kM * (int)rank, kM, warp - 2, 2, lane);
+        const TileAt at = tile_of(i, tiles_n, tiles_t);
+        const int64_t t0 = (int64_t)at.tt * nt;
+        prefetch_rows(p, t0, (int)min((int64_t)nt, p.T - t0), at.tn * 2 * kM + kM * (int)rank, kM, warp - 2, 2, lane);
       }
     }
   } else {
     // ---------------------------------------------------------------- epilogue
-    const int q = warp % 4, half = (warp - 4) / 4;          // TMEM lanes 32q ..
-    int u = 0;
-    for (int64_t i = pair; i < tiles; i += pairs, ++u) {
-      const int b = u & 1;
-      int tn, tt;
-      tile_of(i, tiles_n, tiles_t, tn, tt);
-      const int32_t n = tn * 2 * kM + kM * (int)rank + 32 * q + lane;
-      const int64_t t0 = (int64_t)tt * nt;
-      const int tokens = (int)min((int64_t)nt, p.T - t0);
-      const float bias = p.bias && n < p.N ? __bfloat162float(p.bias[n]) : 0.f;
-      const float ws = F8 && n < p.N ? scale_of(p.ws[n]) : 1.f;
-      // a chunk's operands are loaded before the chunk before it is finished
-      const int64_t at = t0 * p.N + n;
-      Operands<kChunk> ops, next;
-      int c = kChunk * half;
-      if (c < tokens && n < p.N) ops.load(p, at + (int64_t)c * p.N, tokens - c);
-      if (!wait_all(bar(kAccFull + b), (uint32_t)((u >> 1) & 1))) { give_up(); break; }
-      ptx::tc_fence_after();
-      const uint32_t trow = tbase + ((32u * q) << 16) + b * nt;
-#pragma unroll 1
-      for (; c < tokens; c += 2 * kChunk) {
-        float v[kChunk];
-        ptx::tmem_ld_32x32b_x16(trow + c, v);
-        const int after = c + 2 * kChunk;
-        if (after < tokens && n < p.N) next.load(p, at + (int64_t)after * p.N, tokens - after);
-        ptx::tmem_wait_ld();
-        if (n < p.N) finish_tokens<F8, kChunk>(p, v, ops, at + (int64_t)c * p.N, t0 + c, tokens - c, bias, ws);
-        ops = next;
-        __syncwarp();
-      }
-      // this warp has read its part of the accumulator
+    const int q = warp % 4, set = (warp - 4) / 4;          // TMEM lanes 32q ..; every kEpiSets-th chunk
+    struct Tile {
+      int64_t t0;
+      int32_t nw;      // the warp's first feature
+      int tokens;
+    };
+    auto tile_at = [&](int i) {
+      const TileAt at = tile_of(i, tiles_n, tiles_t);
+      const int64_t t0 = (int64_t)at.tt * nt;
+      return Tile{t0, at.tn * 2 * kM + kM * (int)rank + 32 * q, (int)min((int64_t)nt, p.T - t0)};
+    };
+    // this warp has read its part of accumulator b
+    auto release = [&](int b) {
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive_cluster_relaxed(lead(bar(kAccFree + b)));
+    };
+    int u = 0;
+    if (p.octs) {
+      // lane: features n .. n + 7 of tokens lane / 4 and lane / 4 + 8 of a chunk
+      float* turn = reinterpret_cast<float*>(smem + off_turn + (warp - 4) * kTurnBytes);
+      const int slot_bytes = ops * kOpBytes, off_slots = off_ops + (warp - 4) * kOpSlots * slot_bytes;
+      auto op_bar = [&](int slot) { return bar(kOps + (warp - 4) * kOpSlots + slot); };
+      // the next chunk whose operands are to be fetched
+      Tile ft = tile_at(min(pair, tiles - 1));
+      int fi = pair, fc = kChunk * set, fetched = 0, used = 0;
+      auto fetch = [&]() {
+        while (fi < tiles && (fc >= ft.tokens || ft.nw >= p.N)) {
+          fi += pairs;
+          fc = kChunk * set;
+          if (fi < tiles) ft = tile_at(fi);
+        }
+        if (fi >= tiles) return;
+        if (lane == 0) {
+          const int slot = fetched % kOpSlots;
+          const uint32_t dst = sbase + off_slots + slot * slot_bytes;
+          ptx::mbar_arrive_expect_tx(op_bar(slot), (uint32_t)slot_bytes);
+          if (p.mul) ptx::tma_load_2d(dst, &tmMul, op_bar(slot), ft.nw, (int32_t)ft.t0 + fc);
+          if (p.res) ptx::tma_load_2d(dst + slot_bytes - kOpBytes, &tmRes, op_bar(slot), ft.nw, (int32_t)ft.t0 + fc);
+        }
+        ++fetched;
+        fc += kEpiSets * kChunk;
+      };
+      if (ops > 0)
+        for (int k = 0; k < kOpSlots; ++k) fetch();
+      // a tile's constants, and its tokens' scale bytes (lane: tokens lane, lane + 32, ..), are
+      // loaded a tile ahead
+      OctConstants<F8> constants, constants2;
+      uint32_t xb[2] = {0, 0}, xb2[2] = {0, 0};
+      auto prepare = [&](const Tile& t) {
+        constants2.load(p, t.nw + 8 * (lane % 4));
+        if (F8) {
+          uint32_t byte[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) byte[k] = 32 * k + lane < t.tokens ? p.xs[t.t0 + 32 * k + lane] : 0;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            xb2[k] = byte[4 * k] | byte[4 * k + 1] << 8 | byte[4 * k + 2] << 16 | byte[4 * k + 3] << 24;
+        }
+      };
+      Tile t = tile_at(min(pair, tiles - 1)), after = t;
+      prepare(t);
+      bool ok = true;
+      for (int i = pair; i < tiles && ok; i += pairs, ++u) {
+        const int b = u & 1;
+        t = after;
+        constants = constants2;
+        xb[0] = xb2[0];
+        xb[1] = xb2[1];
+        if (i + pairs < tiles) {
+          after = tile_at(i + pairs);
+          prepare(after);
+        }
+        const int32_t n = t.nw + 8 * (lane % 4);
+        const uint32_t trow = tbase + ((32u * q) << 16) + b * nt;
+        if (!wait_all(bar(kAccFull + b), (uint32_t)((u >> 1) & 1))) { give_up(); ok = false; break; }
+        ptx::tc_fence_after();
+#pragma unroll 1
+        for (int c = kChunk * set; c < t.tokens; c += kEpiSets * kChunk) {
+          float v[kChunk];
+          ptx::tmem_ld_32x32b_x16(trow + c, v);
+          const int slot = used % kOpSlots;
+          const bool with_ops = ops > 0 && t.nw < p.N;
+          if (with_ops && !wait_all(op_bar(slot), (uint32_t)((used / kOpSlots) & 1))) {
+            ptx::tmem_wait_ld();
+            give_up();
+            ok = false;
+            break;
+          }
+          const uint4* om = reinterpret_cast<const uint4*>(smem + off_slots + slot * slot_bytes) + lane;
+          const uint4* orr = om + (slot_bytes - kOpBytes) / 16;
+          const uint32_t scales = xb[c >= 128] >> (8 * (c / 32 % 4));      // of tokens c / 32 * 32 + lane
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < kChunk; ++j) turn[j * kTurnPitch + lane] = v[j];
+          __syncwarp();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int j = lane / 4 + 8 * h;
+            const float4* w = reinterpret_cast<const float4*>(turn + j * kTurnPitch + 8 * (lane % 4));
+            const float4 lo = w[0], hi = w[1];
+            float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            uint4 m, r;
+            if (p.mul) m = om[32 * h];
+            if (p.res) r = orr[32 * h];
+            float xs = 1.f;
+            if (F8) xs = scale_of((uint8_t)__shfl_sync(0xffffffffu, scales, c % 32 + j));
+            if (c + j < t.tokens && n < p.N) finish_oct<F8>(p, f, m, r, xs, constants, (t.t0 + c + j) * p.N + n);
+          }
+          __syncwarp();      // the chunk's operands and sums are read
+          if (with_ops) {
+            ++used;
+            fetch();
+          }
+        }
+        release(b);
+      }
+      // operands in flight (after a wait that ran out) land before the CTA may exit
+      for (; used < fetched; ++used)
+        __all_sync(0xffffffffu, ptx::mbar_wait_cluster_timed(op_bar(used % kOpSlots), (uint32_t)((used / kOpSlots) & 1),
+                                                             p.timeout_ns));
+    } else {
+      for (int i = pair; i < tiles; i += pairs, ++u) {
+        const int b = u & 1;
+        const Tile t = tile_at(i);
+        const int32_t n = t.nw + lane;
+        const float bias = p.bias && n < p.N ? __bfloat162float(p.bias[n]) : 0.f;
+        const float ws = F8 && n < p.N ? scale_of(p.ws[n]) : 1.f;
+        const int64_t at = t.t0 * p.N + n;
+        const uint32_t trow = tbase + ((32u * q) << 16) + b * nt;
+        int c = kChunk * set;
+        Operands<kChunk> ops, next;
+        if (c < t.tokens && n < p.N) ops.load(p, at + (int64_t)c * p.N, t.tokens - c);
+        if (!wait_all(bar(kAccFull + b), (uint32_t)((u >> 1) & 1))) { give_up(); break; }
+        ptx::tc_fence_after();
+#pragma unroll 1
+        for (; c < t.tokens; c += kEpiSets * kChunk) {
+          float v[kChunk];
+          ptx::tmem_ld_32x32b_x16(trow + c, v);
+          const int then = c + kEpiSets * kChunk;
+          if (then < t.tokens && n < p.N) next.load(p, at + (int64_t)then * p.N, t.tokens - then);
+          ptx::tmem_wait_ld();
+          if (n < p.N) finish_tokens<F8, kChunk>(p, v, ops, at + (int64_t)c * p.N, t.t0 + c, t.tokens - c, bias, ws);
+          ops = next;
+          __syncwarp();
+        }
+        release(b);
+      }
     }
   }
   __syncthreads();

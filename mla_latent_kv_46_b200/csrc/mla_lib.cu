@@ -1443,6 +1443,8 @@ mla_status launch_linear_split(const void* x, const void* W, mla::lin::Params p,
   CUtensorMap tw, tx;
   if (mla_status s = linear_maps<F8>(&tw, &tx, W, x, p, kM, (uint32_t)nt / 2)) return s;
   if (mla_status s = ensure_smem_attr((const void*)kern, kSmemOfOne)) return s;
+  if (2 * slices > 8)   // above the portable cluster size
+    MLA_CUDA_TRY(cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
   const int64_t tiles_n = ((int64_t)p.N + 2 * kM - 1) / (2 * kM), tiles_t = ((int64_t)p.T + nt - 1) / nt;
   // two CTAs an SM where there are that many and they fit; else one, with all of its memory
   const bool two = 2 * slices * tiles_n * tiles_t > sms && split_smem(nt, 2, slices) <= kSmemOfTwo;
@@ -1460,11 +1462,19 @@ mla_status launch_linear_pair(const void* x, const void* W, mla::lin::Params p, 
   CUtensorMap tw, tx;
   if (mla_status s = linear_maps<F8>(&tw, &tx, W, x, p, kM, (uint32_t)nt / 2)) return s;
   if (mla_status s = ensure_smem_attr((const void*)kern, kSmemOfOne)) return s;
+  const int ops = p.octs ? (p.mul != nullptr) + (p.res != nullptr) : 0;
+  CUtensorMap tm = tx, tr = tx;
+  if (p.octs && p.mul)
+    if (mla_status s = make_store_map_2d(&tm, p.mul, false, p.N, p.T, (uint64_t)p.N * 2, 32, kChunk)) return s;
+  if (p.octs && p.res)
+    if (mla_status s = make_store_map_2d(&tr, p.res, false, p.N, p.T, (uint64_t)p.N * 2, 32, kChunk)) return s;
   p.nt = nt;
-  p.stages = std::min(kMaxStages, (kSmemOfOne - kSmemSlack) / stage_bytes_of(nt));
+  p.stages = std::min(kMaxStages, (kSmemOfOne - pair_smem(nt, 0, ops)) / stage_bytes_of(nt));
   const int64_t tiles = (((int64_t)p.N + 2 * kM - 1) / (2 * kM)) * (((int64_t)p.T + nt - 1) / nt);
+  if (tiles > 0x7FFF0000) return fail(MLA_ERR_UNSUPPORTED, "%s: T=%d N=%d is too large", what, p.T, p.N);
   const unsigned pairs = (unsigned)std::min<int64_t>(tiles, std::max(1, sms / 2));
-  return launch_overlapped(what, kern, dim3(2 * pairs), kPairThreads, pair_smem(nt, p.stages), 0, st, tw, tx, p);
+  return launch_overlapped(what, kern, dim3(2 * pairs), kPairThreads, pair_smem(nt, p.stages, ops), 0, st, tw, tx, tm,
+                           tr, p);
 }
 
 template <bool F8>
@@ -1511,9 +1521,9 @@ mla_status linear(const char* what, bool f8, const void* x, const void* xs, cons
   p.N = N;
   p.K = K;
   p.act = act;
-  p.quads = N % 4 == 0;
+  p.octs = N % 8 == 0 && reinterpret_cast<uintptr_t>(ws) % 8 == 0;
   for (const void* q : {bias, mul, residual, (const void*)out})
-    p.quads = p.quads && reinterpret_cast<uintptr_t>(q) % 8 == 0;
+    p.octs = p.octs && reinterpret_cast<uintptr_t>(q) % 16 == 0;
   p.timeout_ns = g_timeout_ns.load();
   cudaStream_t st = as_stream(stream);
   // what TMA needs: 16-byte aligned operands and rows; the token and feature tile numbers
