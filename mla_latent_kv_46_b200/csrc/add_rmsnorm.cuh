@@ -252,6 +252,8 @@ add_rmsnorm_kernel(const Params p) {
   const int nthr = WARP ? 32 : blockDim.x;
   const int tid = WARP ? (threadIdx.x & 31) : threadIdx.x;
   const int64_t row = WARP ? (int64_t)blockIdx.x * kWarpRows + (threadIdx.x >> 5) : blockIdx.x;
+  ptx::grid_launch_next();
+  ptx::grid_wait();      // from here on this kernel reads and writes global memory
   if (WARP && row >= p.T) return;
   const Row<VE, SHIFTED> at(row, p.T, p.M);
   uint4 xw[ITEMS], rw[ITEMS];
@@ -339,6 +341,10 @@ __global__ void __launch_bounds__(kStreamThreads) add_rmsnorm_stream_kernel(cons
     abort_word = 0;
     for (int s = 0; s < kStages; ++s) ptx::mbar_init(bar(s), 1);
     ptx::fence_mbar_init();
+  }
+  ptx::grid_launch_next();
+  ptx::grid_wait();      // from here on this kernel reads and writes global memory
+  if (tid == 0) {
     for (int s = 0; s < kStages; ++s)
       if (blockIdx.x + (int64_t)s * grid < p.T) fetch(s, blockIdx.x + (int64_t)s * grid);
   }
@@ -424,6 +430,8 @@ __global__ void __launch_bounds__(kStreamThreads) add_rmsnorm_stream_kernel(cons
 template <typename T>
 __global__ void __launch_bounds__(1024) add_rmsnorm_any_kernel(const Params p) {
   __shared__ float red[2][32];
+  ptx::grid_launch_next();
+  ptx::grid_wait();      // from here on this kernel reads and writes global memory
   const int64_t at = (int64_t)blockIdx.x * p.M;
   const T* x = static_cast<const T*>(p.x) + at;
   const T* r = p.r ? static_cast<const T*>(p.r) + at : nullptr;

@@ -533,6 +533,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
   if (warp == 0) {
     // ---------------------------------------------------------------- loads
     const bool leader = ptx::elect_one();
+    const uint64_t w_policy = tiles_t == 1 ? ptx::policy_evict_first() : ptx::policy_evict_normal();   // as above
     int64_t g = 0;       // K blocks of this pair so far
     int s = 0;
     uint32_t parity = 1;
@@ -545,7 +546,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         if (leader) {
           const uint32_t sa = sbase + s * stage_bytes, sb = sa + kABytes;
           if (even) ptx::mbar_arrive_expect_tx(bar(kFull + s), 2 * stage_bytes);
-          ptx::tma_load_2d_pair(sa, &tmW, lead(bar(kFull + s)), kb * kb_elems<F8>(), nrow);
+          ptx::tma_load_2d_pair_hint(sa, &tmW, lead(bar(kFull + s)), kb * kb_elems<F8>(), nrow, w_policy);
           ptx::tma_load_2d_pair(sb, &tmX, lead(bar(kFull + s)), kb * kb_elems<F8>(), trow);
         }
         if (++s == stages) {

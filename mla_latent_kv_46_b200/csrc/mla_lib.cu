@@ -1251,6 +1251,29 @@ int32_t device_sms() {
   return sms;
 }
 
+// Launches with the programmatic attribute: the kernel's set-up may run under the tail of the
+// kernel before it on the stream (it waits for that one before it touches global memory).
+template <class Kernel, class... Args>
+mla_status launch_overlapped(const char* what, Kernel kern, dim3 grid, int threads, int smem, int cluster,
+                             cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  MLA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, args...));
+  return launch_check(what);
+}
+
 // Blocks of a kernel that an SM holds (0: not known), asked for once per kernel,
 // block size, shared memory and device.
 int blocks_per_sm(const void* kernel, int threads, int64_t smem) {
@@ -1277,12 +1300,12 @@ template <typename T, int ITEMS, bool SHIFTED>
 mla_status launch_rms_rows(const mla::rms::Params& p, int granules, cudaStream_t st) {
   if (granules <= 32 * ITEMS) {
     const unsigned blocks = (unsigned)(((int64_t)p.T + mla::rms::kWarpRows - 1) / mla::rms::kWarpRows);
-    mla::rms::add_rmsnorm_kernel<T, ITEMS, true, SHIFTED><<<blocks, 32 * mla::rms::kWarpRows, 0, st>>>(p);
-  } else {
-    const int threads = ((granules + ITEMS - 1) / ITEMS + 31) / 32 * 32;
-    mla::rms::add_rmsnorm_kernel<T, ITEMS, false, SHIFTED><<<(unsigned)p.T, threads, 0, st>>>(p);
+    return launch_overlapped("add_rmsnorm", mla::rms::add_rmsnorm_kernel<T, ITEMS, true, SHIFTED>, dim3(blocks),
+                             32 * mla::rms::kWarpRows, 0, 0, st, p);
   }
-  return launch_check("add_rmsnorm");
+  const int threads = ((granules + ITEMS - 1) / ITEMS + 31) / 32 * 32;
+  return launch_overlapped("add_rmsnorm", mla::rms::add_rmsnorm_kernel<T, ITEMS, false, SHIFTED>, dim3((unsigned)p.T),
+                           threads, 0, 0, st, p);
 }
 
 // Rows in whole and aligned granules, many of them: the streaming kernel. It takes rows of
@@ -1302,8 +1325,8 @@ mla_status launch_rms_stream(const mla::rms::Params& p, cudaStream_t st, bool* d
   const int64_t resident = (int64_t)sms * blocks_per_sm((const void*)kern, threads, smem);
   if (resident == 0 || 2 * (int64_t)p.T < 5 * resident) return MLA_OK;
   *done = true;
-  kern<<<(unsigned)resident, threads, (size_t)smem, st>>>(p, g_timeout_ns.load());
-  return launch_check("add_rmsnorm");
+  return launch_overlapped("add_rmsnorm", kern, dim3((unsigned)resident), threads, (int)smem, 0, st, p,
+                           g_timeout_ns.load());
 }
 
 template <typename T, bool SHIFTED>
@@ -1320,8 +1343,7 @@ mla_status launch_rms(const mla::rms::Params& p, cudaStream_t st) {
   if (granules <= 8 / VE * 1024) return launch_rms_rows<T, 8 / VE, SHIFTED>(p, (int)granules, st);
   if (granules <= 16 / VE * 1024) return launch_rms_rows<T, 16 / VE, SHIFTED>(p, (int)granules, st);
   if (granules <= 32 / VE * mla::rms::kWideThreads) return launch_rms_rows<T, 32 / VE, SHIFTED>(p, (int)granules, st);
-  mla::rms::add_rmsnorm_any_kernel<T><<<(unsigned)p.T, 1024, 0, st>>>(p);
-  return launch_check("add_rmsnorm");
+  return launch_overlapped("add_rmsnorm", mla::rms::add_rmsnorm_any_kernel<T>, dim3((unsigned)p.T), 1024, 0, 0, st, p);
 }
 
 template <typename T>
@@ -1331,8 +1353,7 @@ mla_status launch_rms(const mla::rms::Params& p, cudaStream_t st) {
   for (const void* q : {p.x, p.r, p.gain, (const void*)p.r_out, (const void*)p.y})
     aligned = aligned && reinterpret_cast<uintptr_t>(q) % 16 == 0;
   if (!aligned) {
-    mla::rms::add_rmsnorm_any_kernel<T><<<(unsigned)p.T, 1024, 0, st>>>(p);
-    return launch_check("add_rmsnorm");
+    return launch_overlapped("add_rmsnorm", mla::rms::add_rmsnorm_any_kernel<T>, dim3((unsigned)p.T), 1024, 0, 0, st, p);
   }
   return p.M % VE == 0 ? launch_rms<T, false>(p, st) : launch_rms<T, true>(p, st);
 }
@@ -1412,29 +1433,6 @@ mla_status linear_maps(CUtensorMap* tw, CUtensorMap* tx, const void* W, const vo
 // Shared memory a block may have where an SM is to hold two (each takes 1 KiB more), or one.
 constexpr int kSmemOfTwo = 113 * 1024, kSmemOfOne = 226 * 1024;
 
-// Launches with the programmatic attribute: the kernel's set-up may run under the tail of the
-// kernel before it on the stream (it waits for that one before it touches global memory).
-template <class Kernel, class... Args>
-mla_status launch_overlapped(const char* what, Kernel kern, dim3 grid, int threads, int smem, int cluster,
-                             cudaStream_t st, const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = cluster > 0 ? 2 : 1;
-  MLA_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, args...));
-  return launch_check(what);
-}
-
 template <bool F8>
 mla_status launch_linear_split(const void* x, const void* W, mla::lin::Params p, int nt, int slices, int32_t sms,
                                cudaStream_t st, const char* what) {
@@ -1477,21 +1475,71 @@ mla_status launch_linear_pair(const void* x, const void* W, mla::lin::Params p, 
                            tr, p);
 }
 
+// Which kernel, tokens per tile and K slices. Both kernels' times are estimated from the sizes
+// and the cheapest of a few candidates taken. The constants (microseconds, bytes per
+// microsecond) were fitted to 340 sizes on a B200, T = 1 .. 4096, N = 130 .. 16384, K = 300 ..
+// 16384, both operand types, 3,000 measured variants: the pick is within 1.3 % of the fastest
+// variant on the (geometric) average and 20 % off at worst. What decides, per K block of a CTA:
+// its 16 KiB of W and 64 bytes a token of x through the SM's 105-120 KB/us, or the MMA's 1.2 ns
+// a token; over all CTAs: the operands' bytes from HBM; and behind that the epilogue.
+struct LinearChoice {
+  bool pair;      // the persistent kernel
+  int nt, slices;
+};
+LinearChoice choose_linear(const mla::lin::Params& p, bool f8, int sms) {
+  using namespace mla::lin;
+  const int kblk = (int)(((int64_t)p.K * (f8 ? 1 : 2) + kKBytes - 1) / kKBytes);
+  const int64_t tiles_n = ((int64_t)p.N + 2 * kM - 1) / (2 * kM);
+  const double bytes = ((double)p.T + p.N) * p.K * (f8 ? 1 : 2) +
+                       2.0 * p.T * p.N * (1 + (p.mul != nullptr) + (p.res != nullptr));
+  const double hbm = bytes / 7.7e6, pairs = std::max(1, sms / 2);
+  auto up16 = [](int64_t v) { return (int)((v + 15) / 16 * 16); };
+  LinearChoice best{true, 256, 1};
+  double best_us = 1e30;
+  auto consider = [&](const LinearChoice& c, double us) {
+    if (us < best_us) {
+      best = c;
+      best_us = us;
+    }
+  };
+  auto pair = [&](int nt) {
+    const double waves = std::ceil(tiles_n * std::ceil((double)p.T / nt) / pairs);
+    const double block = std::max((kABytes + 64.0 * nt) / 120e3, 1.2e-3 * nt), epilogue = 1.6 + 0.023 * nt;
+    consider({true, nt, 1}, 3.1 + std::max(waves * std::max(kblk * block, epilogue), hbm) + epilogue);
+  };
+  const int64_t least = ((int64_t)p.T + 255) / 256;      // token tiles of 256
+  for (int64_t j = least; j < least + 4; ++j)
+    if (j == least || up16((p.T + j - 1) / j) >= 48) pair(up16((p.T + j - 1) / j));
+  for (int nt : {64, 96, 128, 160, 192})
+    if (nt < p.T) pair(nt);
+  if (p.T <= 8 * 256 && tiles_n <= 65535)
+    for (int j : {1, 2, 3, 4, 6, 8}) {
+      const int nt = up16((p.T + j - 1) / j);
+      if (nt > 256 || (j > 1 && nt < 32)) continue;
+      const double tiles = tiles_n * std::ceil((double)p.T / nt);
+      for (int slices = 1; slices <= kMaxSlices; slices *= 2) {
+        if (slices > 1 && 2 * slices > kblk) break;
+        // clusters of 2 * slices CTAs that fit at once, at one CTA an SM: GPCs hold 16 to 20 SMs
+        const int fit = slices == 1 ? (int)pairs : slices == 2 ? 36 : slices == 4 ? 14 : 7;
+        const bool two = 2 * slices * tiles > sms && split_smem(nt, 2, slices) <= kSmemOfTwo;
+        if (slices == kMaxSlices && tiles > fit) break;
+        if (split_smem(nt, 1, slices) > kSmemOfOne) continue;
+        const double waves = std::ceil(tiles / (fit * (two ? 2 : 1)));
+        const double share = std::min(two ? 2.0 : 1.0, std::max(1.0, 2 * slices * tiles / sms));   // CTAs at work an SM
+        const double block = std::max({(kABytes + 64.0 * nt) * share / 105e3, 1.2e-3 * nt * share, 0.115});
+        const double tail = 0.9 + (slices > 1 ? 1.4 : 0.0) + 0.0345 * nt / std::min(slices, nt / 16);
+        consider({false, nt, slices}, 8.0 + std::max(waves * std::ceil((double)kblk / slices) * block, hbm) + waves * tail);
+      }
+    }
+  return best;
+}
+
 template <bool F8>
 mla_status linear_tc(const void* x, const void* W, const mla::lin::Params& p, cudaStream_t st, const char* what) {
-  using namespace mla::lin;
   const int32_t sms = device_sms();
-  if (p.T <= 256) {
-    const int nt = (p.T + 15) / 16 * 16;
-    const int64_t tiles = ((int64_t)p.N + 2 * kM - 1) / (2 * kM);
-    const int kblk = (p.K + kb_elems<F8>() - 1) / kb_elems<F8>();
-    // K slices: as many CTAs as the GPU holds at once (two per SM where shared memory allows)
-    const int64_t room = (int64_t)sms * (split_smem(nt, 2, kMaxSlices) <= kSmemOfTwo ? 2 : 1) / 2;
-    int slices = 1;
-    while (2 * slices <= kMaxSlices && 2 * slices * tiles <= room && 4 * slices <= kblk) slices *= 2;
-    return launch_linear_split<F8>(x, W, p, nt, slices, sms, st, what);
-  }
-  return launch_linear_pair<F8>(x, W, p, 256, sms, st, what);
+  const LinearChoice c = choose_linear(p, F8, sms);
+  return c.pair ? launch_linear_pair<F8>(x, W, p, c.nt, sms, st, what)
+                : launch_linear_split<F8>(x, W, p, c.nt, c.slices, sms, st, what);
 }
 
 mla_status linear(const char* what, bool f8, const void* x, const void* xs, const void* W, const void* ws,
@@ -1530,7 +1578,7 @@ mla_status linear(const char* what, bool f8, const void* x, const void* xs, cons
   // within the grid's and the coordinates' 32 bits
   const int32_t pol = g_policy.load();
   const bool tc = reinterpret_cast<uintptr_t>(x) % 16 == 0 && reinterpret_cast<uintptr_t>(W) % 16 == 0 &&
-                  (size_t)K * es % 16 == 0 && T <= 0x7FFFF000 && N <= 65535 * mla::lin::kM;
+                  (size_t)K * es % 16 == 0 && T <= 0x7FFFF000 && N <= 0x7FFFF000;
   if (pol == MLA_POLICY_TCGEN05 && !tc)
     return fail(MLA_ERR_UNSUPPORTED, "%s: the tensor-core kernels need 16-byte aligned rows of x and W", what);
   if (pol != MLA_POLICY_SIMT && tc)
