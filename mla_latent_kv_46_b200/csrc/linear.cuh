@@ -35,22 +35,33 @@ __device__ __forceinline__ float scale_of(uint8_t b) { return __uint_as_float((u
 // exp by ex2.approx and the quotient by rcp.approx, a few units in 2^-22 off (the result is
 // rounded to bf16, 2^-9): a full division took a third of the epilogue's instructions. Sums so
 // negative that e^-v overflows give 0, as the formulas do.
-__device__ __forceinline__ float activate(float v, int act) {
-  switch (act) {
-    case kActSigmoid: return __fdividef(1.f, 1.f + __expf(-v));
-    case kActSilu: return __fdividef(v, 1.f + __expf(-v));
-    case kActGelu: return 0.5f * v * erfcf(-0.70710678118654752f * v);
-    default: return v;
+__device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
+__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + __expf(-v)); }
+__device__ __noinline__ float gelu(float v) { return 0.5f * v * erfcf(-0.70710678118654752f * v); }
+// All of a thread's elements: one branch, straight code behind it (a branch per element of an
+// unrolled epilogue ran out of the instruction cache, as did gelu inlined for each).
+template <int CNT>
+__device__ __forceinline__ void activate(float (&v)[CNT], int act) {
+  if (act == kActSigmoid) {
+#pragma unroll
+    for (int j = 0; j < CNT; ++j) v[j] = sigmoid(v[j]);
+  } else if (act == kActSilu) {
+#pragma unroll
+    for (int j = 0; j < CNT; ++j) v[j] = silu(v[j]);
+  } else if (act == kActGelu) {
+#pragma unroll
+    for (int j = 0; j < CNT; ++j) v[j] = gelu(v[j]);
   }
 }
 
 // One output element from its fp32 sum (8-bit operands: already times both scales).
 __device__ __forceinline__ void finish(const Params& p, float v, int64_t t, int32_t n, float bias) {
   const int64_t at = t * p.N + n;
-  v = activate(v + bias, p.act);
-  if (p.mul) v *= __bfloat162float(p.mul[at]);
-  if (p.res) v += __bfloat162float(p.res[at]);
-  p.out[at] = __float2bfloat16_rn(v);
+  float y[1] = {v + bias};
+  activate(y, p.act);
+  if (p.mul) y[0] *= __bfloat162float(p.mul[at]);
+  if (p.res) y[0] += __bfloat162float(p.res[at]);
+  p.out[at] = __float2bfloat16_rn(y[0]);
 }
 
 // ------------------------------------------------------------------ CUDA cores

@@ -53,21 +53,30 @@ struct Operands {
   }
 };
 
-// Epilogue of those tokens, t0 first, of a feature below N.
+// Every lane's bytes of lanes first .. first + CNT - 1, four to a word.
+template <int WORDS>
+__device__ __forceinline__ void spread_scales(uint32_t mine, int first, uint32_t (&sx)[WORDS]) {
+#pragma unroll
+  for (int k = 0; k < WORDS; ++k) {
+    sx[k] = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sx[k] |= __shfl_sync(0xffffffffu, mine, first + 4 * k + e) << (8 * e);
+  }
+}
+
+// Epilogue of those tokens for a feature below N; sx: byte j of word j / 4 of the tokens' scale
+// bytes (8-bit operands). Two tokens' results are converted at once, and a whole chunk is stored
+// without a test per token: single conversions and the tests were most of this function's time.
 template <bool F8, int CNT>
 __device__ __forceinline__ void finish_tokens(const Params& p, float (&v)[CNT], const Operands<CNT>& o, int64_t at,
-                                              int64_t t0, int tokens, float bias, float ws) {
+                                              int tokens, float bias, float ws, const uint32_t (&sx)[CNT / 4]) {
   if (F8) {
 #pragma unroll
-    for (int j = 0; j < CNT; ++j)
-      if (j < tokens) v[j] = v[j] * ws * scale_of(p.xs[t0 + j]);
+    for (int j = 0; j < CNT; ++j) v[j] = v[j] * ws * scale_of((uint8_t)(sx[j / 4] >> (8 * (j % 4))));
   }
 #pragma unroll
   for (int j = 0; j < CNT; ++j) v[j] += bias;
-  if (p.act != kActNone) {
-#pragma unroll
-    for (int j = 0; j < CNT; ++j) v[j] = activate(v[j], p.act);
-  }
+  activate(v, p.act);
   if (p.mul) {
 #pragma unroll
     for (int j = 0; j < CNT; ++j) v[j] *= __bfloat162float(o.m[j]);
@@ -76,9 +85,18 @@ __device__ __forceinline__ void finish_tokens(const Params& p, float (&v)[CNT], 
 #pragma unroll
     for (int j = 0; j < CNT; ++j) v[j] += __bfloat162float(o.r[j]);
   }
+  __nv_bfloat16* out = p.out + at;
+  __nv_bfloat162 two[CNT / 2];
 #pragma unroll
-  for (int j = 0; j < CNT; ++j)
-    if (j < tokens) p.out[at + (int64_t)j * p.N] = __float2bfloat16_rn(v[j]);
+  for (int j = 0; j < CNT / 2; ++j) two[j] = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+  if (tokens >= CNT) {
+#pragma unroll
+    for (int j = 0; j < CNT; ++j, out += p.N) *out = j % 2 ? two[j / 2].y : two[j / 2].x;
+  } else {
+#pragma unroll
+    for (int j = 0; j < CNT; ++j, out += p.N)
+      if (j < tokens) *out = j % 2 ? two[j / 2].y : two[j / 2].x;
+  }
 }
 
 // Where N and every pointer allow it (p.octs), the epilogue moves eight neighbouring features
@@ -107,10 +125,7 @@ __device__ __forceinline__ void finish_oct(const Params& p, float (&v)[8], const
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] += f[j];
   }
-  if (p.act != kActNone) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = activate(v[j], p.act);
-  }
+  activate(v, p.act);
   if (p.mul) {
     f8::unpack8(mul, f);
 #pragma unroll
@@ -341,7 +356,7 @@ __global__ void __launch_bounds__(kSplitThreads) linear_split_kernel(const __gri
   }
   __syncthreads();
   if (slices > 1) ptx::cluster_sync();   // every slice's sums are here; nothing remote is touched from now on
-  if (done && slice < chunks && n < p.N) {
+  if (done && slice < chunks && n < p.N && p.octs) {
     // the slices' sums added in their order, for this CTA's tokens: whole chunks, but for the
     // last of all
     const float* part = reinterpret_cast<const float*>(smem);
@@ -351,71 +366,63 @@ __global__ void __launch_bounds__(kSplitThreads) linear_split_kernel(const __gri
     auto token_of = [&](int i) { return t0 + (int64_t)(i / kChunk * slices + slice) * kChunk + i % kChunk; };
     constexpr int kBatch = 4;   // tokens whose operands are loaded before the first is finished: out may
                                 // be mul's or residual's buffer, so no load moves above an earlier store
-    if (p.octs) {
-      constexpr int kStep = kSplitThreads / kOcts;
-      for (int i0 = tid / kOcts; i0 < held; i0 += kBatch * kStep) {
-        uint4 m[kBatch], r[kBatch];
-        float xs[kBatch];
+    constexpr int kStep = kSplitThreads / kOcts;
+    for (int i0 = tid / kOcts; i0 < held; i0 += kBatch * kStep) {
+      uint4 m[kBatch], r[kBatch];
+      float xs[kBatch];
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const int i = i0 + b * kStep;
-          if (i < held) {
-            const int64_t t = token_of(i), at = t * p.N + n;
-            if (F8) xs[b] = scale_of(p.xs[t]);
-            if (p.mul) m[b] = *reinterpret_cast<const uint4*>(p.mul + at);
-            if (p.res) r[b] = *reinterpret_cast<const uint4*>(p.res + at);
-          }
-        }
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const int i = i0 + b * kStep;
-          if (i < held) {
-            float v[8] = {};
-#pragma unroll
-            for (int s = 0; s < kMaxSlices; ++s)
-              if (s < slices) {
-                const float4* w = reinterpret_cast<const float4*>(part + s * stride + i * kM + 8 * (tid % kOcts));
-                const float4 lo = w[0], hi = w[1];
-                v[0] += lo.x;
-                v[1] += lo.y;
-                v[2] += lo.z;
-                v[3] += lo.w;
-                v[4] += hi.x;
-                v[5] += hi.y;
-                v[6] += hi.z;
-                v[7] += hi.w;
-              }
-            finish_oct<F8>(p, v, m[b], r[b], xs[b], constants, token_of(i) * p.N + n);
-          }
+      for (int b = 0; b < kBatch; ++b) {
+        const int i = i0 + b * kStep;
+        if (i < held) {
+          const int64_t t = token_of(i), at = t * p.N + n;
+          if (F8) xs[b] = scale_of(p.xs[t]);
+          if (p.mul) m[b] = *reinterpret_cast<const uint4*>(p.mul + at);
+          if (p.res) r[b] = *reinterpret_cast<const uint4*>(p.res + at);
         }
       }
-    } else {
-      constexpr int kStep = kSplitThreads / kM;
-      for (int i0 = tid / kM; i0 < held; i0 += kBatch * kStep) {
-        float v[kBatch], m[kBatch], r[kBatch];
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const int i = i0 + b * kStep;
-          if (i < held) {
-            const int64_t t = token_of(i), at = t * p.N + n;
-            v[b] = 0.f;
-            for (int s = 0; s < slices; ++s) v[b] += part[s * stride + i * kM + tid % kM];
-            if (F8) v[b] = v[b] * ws * scale_of(p.xs[t]);
-            if (p.mul) m[b] = __bfloat162float(p.mul[at]);
-            if (p.res) r[b] = __bfloat162float(p.res[at]);
-          }
-        }
+      for (int b = 0; b < kBatch; ++b) {
+        const int i = i0 + b * kStep;
+        if (i < held) {
+          float v[8] = {};
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const int i = i0 + b * kStep;
-          if (i < held) {
-            float y = activate(v[b] + bias, p.act);
-            if (p.mul) y *= m[b];
-            if (p.res) y += r[b];
-            p.out[token_of(i) * p.N + n] = __float2bfloat16_rn(y);
-          }
+          for (int s = 0; s < kMaxSlices; ++s)
+            if (s < slices) {
+              const float4* w = reinterpret_cast<const float4*>(part + s * stride + i * kM + 8 * (tid % kOcts));
+              const float4 lo = w[0], hi = w[1];
+              v[0] += lo.x;
+              v[1] += lo.y;
+              v[2] += lo.z;
+              v[3] += lo.w;
+              v[4] += hi.x;
+              v[5] += hi.y;
+              v[6] += hi.z;
+              v[7] += hi.w;
+            }
+          finish_oct<F8>(p, v, m[b], r[b], xs[b], constants, token_of(i) * p.N + n);
         }
       }
+    }
+  }
+  if (done && slice < chunks && !p.octs) {
+    // one feature and a chunk of tokens per thread, a chunk's operands all in flight at once
+    const float* part = reinterpret_cast<const float*>(smem);
+    for (int k = tid / kM; slice + k * slices < chunks; k += kSplitThreads / kM) {
+      const int64_t t = t0 + (int64_t)(slice + k * slices) * kChunk;
+      const int left = (int)min((int64_t)kChunk, t0 + tokens - t);
+      const int64_t at = t * p.N + n;
+      Operands<kChunk> ops;
+      if (n < p.N) ops.load(p, at, left);
+      uint32_t sx[kChunk / 4] = {};
+      if (F8) {
+        const uint32_t mine = lane < left ? p.xs[t + lane] : 0;
+        spread_scales(mine, 0, sx);
+      }
+      float v[kChunk] = {};
+      for (int s = 0; s < slices; ++s)
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j) v[j] += part[((s * per + k) * kChunk + j) * kM + tid % kM];
+      if (n < p.N) finish_tokens<F8, kChunk>(p, v, ops, at, left, bias, ws, sx);
     }
   }
   ptx::tc_fence_before();
@@ -448,6 +455,16 @@ static_assert(8 * (2 * kMaxStages + 4 + kEpiWarps * kOpSlots) + 16 <= kPairBarBy
 __host__ __device__ constexpr int pair_extra(int ops) { return kEpiWarps * (kTurnBytes + ops * kOpSlots * kOpBytes); }
 __host__ __device__ constexpr int pair_smem(int nt, int stages, int ops) {
   return stages * stage_bytes_of(nt) + pair_extra(ops) + kPairSlack;
+}
+
+// A tile's scale bytes of x, four to a word: byte k of word h is token 128 h + 32 k + lane's.
+__device__ __forceinline__ void load_scales(const Params& p, int64_t t0, int tokens, int lane, uint32_t (&xb)[2]) {
+  uint32_t byte[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) byte[k] = 32 * k + lane < tokens ? p.xs[t0 + 32 * k + lane] : 0;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    xb[k] = byte[4 * k] | byte[4 * k + 1] << 8 | byte[4 * k + 2] << 16 | byte[4 * k + 3] << 24;
 }
 
 constexpr int kGroupT = 8;   // token tiles that share a sweep over the feature tiles
@@ -660,14 +677,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
       uint32_t xb[2] = {0, 0}, xb2[2] = {0, 0};
       auto prepare = [&](const Tile& t) {
         constants2.load(p, t.nw + 8 * (lane % 4));
-        if (F8) {
-          uint32_t byte[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) byte[k] = 32 * k + lane < t.tokens ? p.xs[t.t0 + 32 * k + lane] : 0;
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            xb2[k] = byte[4 * k] | byte[4 * k + 1] << 8 | byte[4 * k + 2] << 16 | byte[4 * k + 3] << 24;
-        }
+        if (F8) load_scales(p, t.t0, t.tokens, lane, xb2);
       };
       Tile t = tile_at(min(pair, tiles - 1)), after = t;
       prepare(t);
@@ -737,6 +747,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         const int32_t n = t.nw + lane;
         const float bias = p.bias && n < p.N ? __bfloat162float(p.bias[n]) : 0.f;
         const float ws = F8 && n < p.N ? scale_of(p.ws[n]) : 1.f;
+        uint32_t xb[2] = {0, 0};
+        if (F8) load_scales(p, t.t0, t.tokens, lane, xb);
         const int64_t at = t.t0 * p.N + n;
         const uint32_t trow = tbase + ((32u * q) << 16) + b * nt;
         int c = kChunk * set;
@@ -751,7 +763,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
           const int then = c + kEpiSets * kChunk;
           if (then < t.tokens && n < p.N) next.load(p, at + (int64_t)then * p.N, t.tokens - then);
           ptx::tmem_wait_ld();
-          if (n < p.N) finish_tokens<F8, kChunk>(p, v, ops, at + (int64_t)c * p.N, t.t0 + c, t.tokens - c, bias, ws);
+          uint32_t sx[kChunk / 4] = {};
+          if (F8) spread_scales(xb[c >= 128] >> (8 * (c / 32 % 4)) & 0xFFu, c % 32, sx);   // of tokens c / 32 * 32 + lane
+          if (n < p.N)
+            finish_tokens<F8, kChunk>(p, v, ops, at + (int64_t)c * p.N, t.tokens - c, bias, ws, sx);
           ops = next;
           __syncwarp();
         }
