@@ -269,6 +269,26 @@ def prologue_inputs(spec: WorkloadSpec, T: int, M: int, seed: int = 0) -> dict:
     return dict(hidden=_store(spec, hidden), W_DKV=_store(spec, w), kv_gain=_store(spec, gain))
 
 
+def layer_inputs(spec: WorkloadSpec, T: int, M: int, seed: int = 0, gate: bool = True) -> dict:
+    """Seeded inputs of a whole attention layer's step around the workload (storage dtype, bf16):
+    the layer input x and the residual stream [T, M] ~ N(0, 1), the norm's gain, and the
+    projections out x in, ~ N(0, 1/in) so that every intermediate has unit scale."""
+    g = _rng(seed, 8)
+    n_out = spec.H * spec.Dv
+
+    def normal(std, *shape):
+        return _store(spec, (g.standard_normal(shape) * std).astype(np.float32))
+    w = {"x": normal(1.0, T, M), "residual": normal(1.0, T, M),
+         "gain": _store(spec, (1 + 0.1 * g.standard_normal(M)).astype(np.float32)),
+         "W_QN": normal(M ** -0.5, spec.H * spec.Dn, M), "W_QR": normal(M ** -0.5, spec.H * spec.Dr, M),
+         "W_O": normal(n_out ** -0.5, M, n_out)}
+    if gate:
+        w["W_G"] = normal(M ** -0.5, n_out, M)
+    pro = prologue_inputs(spec, T, M, seed)
+    w["W_DKV"], w["kv_gain"] = pro["W_DKV"], pro["kv_gain"]
+    return w
+
+
 def latent_outputs(spec: WorkloadSpec, T: int, seed: int = 0, fp32: bool = False) -> np.ndarray:
     """Seeded stand-in for a latent attention output, [T, H, R]: entries N(0, 0.1^2),
     in the workload's storage dtype, or as float32 values when `fp32`."""

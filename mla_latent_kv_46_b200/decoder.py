@@ -151,6 +151,102 @@ class DecodeStep:
         return int(append) + 3 + int(self.info.num_parts > 0) + int(self.fp8)
 
 
+class LayerStep:
+    """One decode step of a whole attention layer, from the residual stream to the residual
+    stream, around a DecodeStep: residual addition and RMS norm, query projections, the
+    cache-write prologue (which also turns the rope queries), absorption, attention, combine,
+    output up-projection, the optional output gate, and Wo with the residual's addition.
+
+    `weights` (torch tensors on the step's device, bf16): gain [M], W_QN [H*Dn, M], W_QR
+    [H*Dr, M], W_DKV [R+Dr, M], kv_gain [R], W_O [M, H*Dv] and, for a gated layer, W_G
+    [H*Dv, M] (each out x in). projections="fp8": the query, gate and output projections
+    run in 8 bits, their weights quantised here once; the cache write keeps bf16 rows.
+    The step's cache must be the bf16 one (the prologue writes bf16 rows)."""
+
+    def __init__(self, step: DecodeStep, weights: dict, projections: str = "bf16", eps: float = 1e-6,
+                 rope_base: float = 10000.0):
+        if step.fp8:
+            raise ValueError("LayerStep needs the bf16 cache: the cache-write prologue writes bf16 rows")
+        if projections not in ("bf16", "fp8"):
+            raise ValueError(f"unknown projections {projections!r}")
+        spec = step.spec
+        self.step = step
+        self.w = weights
+        self.fp8 = projections == "fp8"
+        self.eps, self.rope_base = eps, rope_base
+        self.M = int(weights["gain"].numel())
+        self.T, self.n_out = step.T, spec.H * spec.Dv
+        self.n_nope, self.n_rope = spec.H * spec.Dn, spec.H * spec.Dr
+        self.gated = weights.get("W_G") is not None
+        d = step.device
+
+        def empty(*shape, dtype=torch.bfloat16):
+            return torch.empty(shape, dtype=dtype, device=d)
+        self.residual = empty(self.T, self.M)     # the stream after the addition
+        self.hidden = empty(self.T, self.M)       # its normalised rows
+        self.y = empty(self.T, self.M)            # the stream after the layer
+        self.ws_bytes = mla.mla_cache_write_workspace_size(self.T, self.M)
+        self.workspace = empty(max(self.ws_bytes, 16), dtype=torch.uint8)
+        if self.fp8:
+            self.codes, self.scales = empty(self.T, self.M, dtype=torch.uint8), empty(self.T, dtype=torch.uint8)
+            self.out_codes = empty(self.T, self.n_out, dtype=torch.uint8)
+            self.out_scales = empty(self.T, dtype=torch.uint8)
+            self.w8 = {}
+            for name in ("W_QN", "W_QR", "W_O") + (("W_G",) if self.gated else ()):
+                n, k = weights[name].shape
+                c, s = empty(n, k, dtype=torch.uint8), empty(n, dtype=torch.uint8)
+                mla.mla_quantize_fp8(weights[name], c, s, n, k, mla.MLA_BF16)
+                self.w8[name] = (c, s)
+
+    def _project(self, name, out, n, act=mla.MLA_ACT_NONE, mul=None, stream=None):
+        """out = mul * act(hidden W^T)."""
+        if self.fp8:
+            mla.mla_linear_fp8(self.codes, self.scales, *self.w8[name], None, mul, None, out, self.T, n, self.M, act,
+                               stream)
+        else:
+            mla.mla_linear(self.hidden, self.w[name], None, mul, None, out, self.T, n, self.M, act, stream)
+
+    def norm_and_queries(self, x, residual, stream=None):
+        """residual + x and its normalised rows, and the step's queries from them."""
+        st = self.step
+        if self.fp8:
+            mla.mla_add_rmsnorm_fp8(x, residual, self.w["gain"], self.residual, self.hidden, self.codes, self.scales,
+                                    self.T, self.M, self.eps, mla.MLA_BF16, stream)
+        else:
+            mla.mla_add_rmsnorm(x, residual, self.w["gain"], self.residual, self.hidden, self.T, self.M, self.eps,
+                                mla.MLA_BF16, stream)
+        self._project("W_QN", st.q_nope, self.n_nope, stream=stream)
+        self._project("W_QR", st.q_rope, self.n_rope, stream=stream)
+
+    def cache_write(self, stream=None):
+        st = self.step
+        mla.mla_cache_write(self.hidden, self.w["W_DKV"], self.w["kv_gain"], self.M, st.kv, st.block_table,
+                            st.seq_lens, st.B, st.q_len, st.max_pages, st.num_pages, st.q_rope, self.eps,
+                            self.rope_base, self.workspace, self.ws_bytes, st.dims, stream)
+
+    def gate_and_output(self, stream=None):
+        """y = residual + Wo(gate * attention)."""
+        st = self.step
+        if self.gated:
+            self._project("W_G", st.out, self.n_out, mla.MLA_ACT_SIGMOID, st.out, stream)     # in place
+        if self.fp8:
+            mla.mla_quantize_fp8(st.out, self.out_codes, self.out_scales, self.T, self.n_out, mla.MLA_BF16, stream)
+            mla.mla_linear_fp8(self.out_codes, self.out_scales, *self.w8["W_O"], None, None, self.residual, self.y,
+                               self.T, self.M, self.n_out, mla.MLA_ACT_NONE, stream)
+        else:
+            mla.mla_linear(st.out, self.w["W_O"], None, None, self.residual, self.y, self.T, self.M, self.n_out,
+                           mla.MLA_ACT_NONE, stream)
+
+    def run(self, x, residual, stream=None):
+        """The whole step for the new tokens' layer input x and residual stream [T, M];
+        returns y [T, M], the residual stream after the layer (this object's buffer)."""
+        self.norm_and_queries(x, residual, stream)
+        self.cache_write(stream)
+        self.step.run(append=False, stream=stream)
+        self.gate_and_output(stream)
+        return self.y
+
+
 class HostInputs:
     """Pinned host copies of one step's per-step inputs and its result."""
 

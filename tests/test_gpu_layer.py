@@ -398,3 +398,167 @@ def test_two_runs_are_bitwise_equal():
         x, W = bf16(rng.standard_normal((T, K))), bf16(rng.standard_normal((N, K)))
         a = run_linear(x, W, None, None, None, T, N, K)
         assert torch.equal(a, run_linear(x, W, None, None, None, T, N, K))
+
+
+# ----------------------------------------------------------------------------- a layer's step, all of it
+def layer_case(H, q_len, lens, M, projections, gate, seed=21):
+    spec = wl.WorkloadSpec(name="layer", B=0, H=H, R=512, Dr=64, Dn=128, Dv=128, q_len=q_len, dtype="bf16",
+                           seq_len=None, w_std=1.0 / np.sqrt(512))
+    w = wl.make(spec, seed=seed, seq_lens=lens, new_rows_in_cache=False)
+    st = dec.DecodeStep(w, sms=8)
+    pin = wl.layer_inputs(spec, st.T, M, seed=seed, gate=gate)
+    t = {k: dec.to_torch(v, st.device) for k, v in pin.items()}
+    lay = dec.LayerStep(st, {k: v for k, v in t.items() if k not in ("x", "residual")}, projections=projections)
+    return spec, w, st, t, lay
+
+
+def near(got, ref, terms, what):
+    """bf16 output of an fp32 sum of `terms` products whose operands are exact: half a step,
+    and 2^-23 of the sum of magnitudes per addition (bounded by terms times the largest output)."""
+    bound = 2.0 ** -8 * np.abs(ref) + terms * 2.0 ** -23 * max(1.0, np.abs(ref).max()) * np.sqrt(terms)
+    err = np.abs(got - ref)
+    assert np.all(err <= bound), f"{what}: worst {np.max(err / bound):.3f} of the bound"
+
+
+@pytest.mark.parametrize("projections,gate,H,q_len,lens,M", [
+    ("bf16", True, 64, 1, [70, 5, 129, 1], 1024), ("fp8", True, 64, 1, [70, 64, 333], 1024),
+    ("bf16", False, 128, 2, [130, 2, 65], 576), ("fp8", False, 128, 1, [40], 7168)])
+def test_layer_step_matches_the_oracle_stage_by_stage(projections, gate, H, q_len, lens, M):
+    """The run as a layer uses it: norm, query projections, cache write, attention, gate, Wo.
+    Every stage against the oracle on the values that the stage before it stored."""
+    spec, w, st, t, lay = layer_case(H, q_len, lens, M, projections, gate)
+    lay.norm_and_queries(t["x"], t["residual"])
+    ref_s, ref_h = layer.add_rmsnorm(host(t["x"]), host(t["residual"]), host(t["gain"]), 1e-6)
+    check_rounded(host(lay.residual), ref_s, 2.0 ** -8, "residual")
+    check_rounded(host(lay.hidden), ref_h, 2.0 ** -8, "hidden")
+
+    def weight(name):
+        if projections == "bf16":
+            return host(t[name])
+        c, s = (v.cpu().numpy() for v in lay.w8[name])
+        want_c, want_s = fp8.quantise_rows(host(t[name]))
+        assert np.array_equal(c, want_c) and np.array_equal(s, want_s)
+        return fp8.dequantise_rows(c, s)
+    if projections == "fp8":
+        check_codes(lay.codes, lay.scales, ref_h)
+        hid = fp8.dequantise_rows(lay.codes.cpu().numpy(), lay.scales.cpu().numpy())
+    else:
+        hid = host(lay.hidden)
+    T = st.T
+    near(host(st.q_nope).reshape(T, -1), layer.linear(hid, weight("W_QN")), M, "q_nope")
+    near(host(st.q_rope).reshape(T, -1), layer.linear(hid, weight("W_QR")), M, "q_rope")
+    q_rope = host(st.q_rope)
+    lay.cache_write()
+    pos = orc.token_positions(lens, q_len)
+    rows = orc.cache_write_rows(host(lay.hidden), host(t["W_DKV"]), host(t["kv_gain"]), pos, spec.R, eps=1e-6)
+    kv = host(st.kv)
+    for i, p in enumerate(pos):
+        row = kv[int(w["block_table"][i // q_len][p // 64]), p % 64]
+        assert np.all(np.abs(row - rows[i]) <= 2e-3 + 1e-2 * np.abs(rows[i]))
+    turned = orc.rope(q_rope, pos[:, None])
+    assert np.all(np.abs(host(st.q_rope) - turned) <= 2e-3 + 1e-2 * np.abs(turned))
+    st.run(append=False)
+    ref = orc.decode_absorbed(host(st.q_nope), host(st.q_rope), kv, w["block_table"], np.asarray(lens), host(st.W_UK),
+                              host(st.W_UV), spec.scale, q_len=q_len, intermediates="q_lat")["out"]
+    att = host(st.out)
+    assert np.all(np.abs(att - ref.reshape(att.shape)) <= 2e-3 + 1e-2 * np.abs(ref.reshape(att.shape)))
+    lay.gate_and_output()
+    mla.mla_check_status()
+    if gate:
+        want = layer.linear(hid, weight("W_G"), mul=att.reshape(T, -1), act="sigmoid")
+        near(host(st.out).reshape(T, -1), want, M, "gate")
+    o = host(st.out).reshape(T, -1)
+    if projections == "fp8":
+        want_c, want_s = fp8.quantise_rows(o)
+        assert np.array_equal(lay.out_codes.cpu().numpy(), want_c)
+        o = fp8.dequantise_rows(want_c, want_s)
+    near(host(lay.y), layer.linear(o, weight("W_O"), residual=host(lay.residual)), H * 128, "y")
+
+
+@pytest.mark.parametrize("projections", ["bf16", "fp8"])
+def test_layer_step_replays_from_a_graph(projections):
+    """One captured step replayed twice equals the eager one bitwise, with new inputs in the same
+    buffers the second time."""
+    spec, w, st, t, lay = layer_case(64, 1, [70, 5, 129, 1], 1024, projections, True)
+    x, res = t["x"].clone(), t["residual"].clone()
+    kv0 = st.kv.clone()
+
+    def eager(a, b):
+        st.kv.copy_(kv0)
+        return lay.run(a, b).clone(), st.kv.clone()
+    want1 = eager(t["x"], t["residual"])
+    want2 = eager(t["residual"], t["x"] * 2)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        lay.run(x, res)
+    for a, b, want in ((t["x"], t["residual"], want1), (t["residual"], t["x"] * 2, want2)):
+        x.copy_(a)
+        res.copy_(b)
+        st.kv.copy_(kv0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(lay.y, want[0]) and torch.equal(st.kv, want[1])
+
+
+def test_layer_step_refuses_the_8_bit_cache():
+    spec = wl.WorkloadSpec(name="layer8", B=0, H=64, R=512, Dr=64, Dn=128, Dv=128, q_len=1, dtype="bf16", seq_len=None,
+                           w_std=1.0 / np.sqrt(512))
+    st = dec.DecodeStep(wl.make(spec, seed=1, seq_lens=[5]), cache="fp8")
+    with pytest.raises(ValueError):
+        dec.LayerStep(st, {"gain": torch.ones(64, device=DEV)})
+
+
+# ----------------------------------------------------------------------------- streams
+def test_calls_on_two_streams_at_once():
+    """No workspace and no state is shared: calls that overlap on the GPU give what they give alone."""
+    rng = np.random.default_rng(12)
+    jobs = []
+    for T, N, K in ((5, 2000, 4096), (900, 1111, 1000), (130, 4096, 2048), (2000, 700, 512)):
+        x, W, r = (bf16(rng.standard_normal(s)) for s in ((T, K), (N, K), (T, N)))
+        jobs.append((x, W, r, T, N, K, run_linear(x, W, None, None, r, T, N, K, "silu")))
+    xs, rs, gain = norm_inputs(1500, 7168, "bf16", seed=3)
+    want_ro, want_y, _, _ = run_norm(xs, rs, gain, 1500, 7168, "bf16", False)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        outs = []
+        for i, (x, W, r, T, N, K, _) in enumerate(jobs):
+            o = torch.empty(T, N, dtype=torch.bfloat16, device=DEV)
+            outs.append(o)
+            mla.mla_linear(x, W, None, None, r, o, T, N, K, mla.MLA_ACT_SILU, stream=streams[i % 2])
+        ro, y = torch.empty_like(xs), torch.empty_like(xs)
+        mla.mla_add_rmsnorm(xs, rs, gain, ro, y, 1500, 7168, 1e-6, mla.MLA_BF16, stream=streams[2])
+        torch.cuda.synchronize()
+        for o, j in zip(outs, jobs):
+            assert torch.equal(o, j[6])
+        assert torch.equal(ro, want_ro) and torch.equal(y, want_y)
+
+
+def test_dependent_calls_in_a_row():
+    """Back-to-back calls where each reads what the one before it wrote (their launches overlap:
+    the second kernel may start before the first has ended), and overwrites what it read."""
+    rng = np.random.default_rng(13)
+    T, M = 64, 1024
+    x, r = bf16(rng.standard_normal((T, M))), bf16(rng.standard_normal((T, M)))
+    gain, W = bf16(1 + 0.1 * rng.standard_normal(M)), bf16(rng.standard_normal((M, M)) / 32)
+
+    def chain(sync):
+        a, b = x.clone(), r.clone()
+        h, y = torch.empty_like(x), torch.empty_like(x)
+        for _ in range(40):
+            mla.mla_add_rmsnorm(a, b, gain, b, h, T, M, 1e-6, mla.MLA_BF16)
+            if sync:
+                torch.cuda.synchronize()
+            mla.mla_linear(h, W, None, None, None, y, T, M, M, mla.MLA_ACT_SILU)
+            if sync:
+                torch.cuda.synchronize()
+            mla.mla_linear(y, W, None, None, h, a, T, M, M, mla.MLA_ACT_NONE)
+            if sync:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return a, b
+    want = chain(True)
+    for _ in range(5):
+        got = chain(False)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
