@@ -398,7 +398,8 @@ __global__ void __launch_bounds__(kStreamThreads) add_rmsnorm_stream_kernel(cons
         for (int k = 0; k < kStages; ++k) {
           const int b = (s + k) % kStages;
           if (row + (int64_t)k * grid < p.T)
-            ptx::mbar_wait_cluster_timed(bar(b), b < s ? parity ^ 1u : parity, timeout_ns);
+            ptx::mbar_wait_cluster_timed(bar(b), b < s ? parity ^ 1u : parity,
+                                         timeout_ns > 10000000ull ? timeout_ns : 10000000ull);
         }
       }
       return;

@@ -163,6 +163,9 @@ __device__ __forceinline__ void prefetch_rows(const Params& p, int64_t t0, int c
 
 // ------------------------------------------------------------------ shared by both kernels
 constexpr int kMaxStages = 12;
+// How long a kernel that gave up waits for its own copies and MMAs in flight, which land
+// within microseconds, however short the caller's bound on waits is.
+__device__ __forceinline__ uint64_t drain_ns(const Params& p) { return p.timeout_ns > 10000000ull ? p.timeout_ns : 10000000ull; }
 constexpr int kBarBytes = 256;       // barriers and two words behind the ring
 constexpr int kSmemSlack = kBarBytes + 1024;
 static_assert(8 * (2 * kMaxStages + 4) + 16 <= kBarBytes, "barriers");
@@ -208,9 +211,9 @@ __global__ void __launch_bounds__(kSplitThreads) linear_split_kernel(const __gri
   const uint32_t r = blockIdx.x & 1;      // CTA of its pair; cluster rank 2 slice + r
   const bool even = r == 0;
   const int off_bar = split_ring(nt, stages, slices);
-  // barriers: full (even CTA: both CTAs' loads), empty and done (each CTA)
+  // barriers: full (even CTA: both CTAs' loads), empty and done (each CTA), drain (even CTA)
   auto bar = [&](int i) { return sbase + off_bar + 8u * i; };
-  const int kFull = 0, kEmpty = stages, kDone = 2 * stages, off_misc = off_bar + 8 * (2 * stages + 2);
+  const int kFull = 0, kEmpty = stages, kDone = 2 * stages, kDrain = 2 * stages + 1, off_misc = off_bar + 8 * (2 * stages + 2);
   auto lead = [&](uint32_t a) { return ptx::map_peer(a, 2 * slice); };
   const uint16_t both = (uint16_t)(3u << (2 * slice));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + off_misc + 8);
@@ -228,6 +231,7 @@ __global__ void __launch_bounds__(kSplitThreads) linear_split_kernel(const __gri
       ptx::mbar_init(bar(kEmpty + s), 1);
     }
     ptx::mbar_init(bar(kDone), 1);
+    ptx::mbar_init(bar(kDrain), 1);
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&tmW);
     ptx::prefetch_tmap(&tmX);
@@ -281,7 +285,7 @@ __global__ void __launch_bounds__(kSplitThreads) linear_split_kernel(const __gri
     // the loads in flight land before the pair may exit (both CTAs' count on these barriers)
     if (even)
       for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
-        __all_sync(0xffffffffu, ptx::mbar_wait_cluster_timed(bar(kFull + i % stages), (i / stages) & 1, p.timeout_ns));
+        __all_sync(0xffffffffu, ptx::mbar_wait_cluster_timed(bar(kFull + i % stages), (i / stages) & 1, drain_ns(p)));
   } else if (warp == 1 && even) {
     // ---------------------------------------------------------------- MMA issuer
     const bool leader = ptx::elect_one();
@@ -308,6 +312,10 @@ __global__ void __launch_bounds__(kSplitThreads) linear_split_kernel(const __gri
         s = 0;
         parity ^= 1;
       }
+    }
+    if (!ok) {      // the MMAs issued so far end before the pair's memory goes
+      if (leader) ptx::umma_commit_pair(bar(kDrain), (uint16_t)(1u << (2 * slice)));
+      __all_sync(0xffffffffu, ptx::mbar_wait_cluster_timed(bar(kDrain), 0, drain_ns(p)));
     }
   }
 
@@ -451,7 +459,7 @@ constexpr int kOpBytes = kChunk * 32 * 2;      // one operand of a warp's chunk:
 // and its operand slots
 constexpr int kTurnPitch = 36, kTurnBytes = kChunk * kTurnPitch * 4;
 constexpr int kPairBarBytes = 512, kPairSlack = kPairBarBytes + 1024;
-static_assert(8 * (2 * kMaxStages + 4 + kEpiWarps * kOpSlots) + 16 <= kPairBarBytes, "barriers");
+static_assert(8 * (2 * kMaxStages + 5 + kEpiWarps * kOpSlots) + 16 <= kPairBarBytes, "barriers");
 __host__ __device__ constexpr int pair_extra(int ops) { return kEpiWarps * (kTurnBytes + ops * kOpSlots * kOpBytes); }
 __host__ __device__ constexpr int pair_smem(int nt, int stages, int ops) {
   return stages * stage_bytes_of(nt) + pair_extra(ops) + kPairSlack;
@@ -498,7 +506,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
   const int off_bar = stages * (int)stage_bytes + pair_extra(ops);
   auto bar = [&](int i) { return sbase + off_bar + 8u * i; };
   const int kFull = 0, kEmpty = stages, kAccFull = 2 * stages, kAccFree = 2 * stages + 2;
-  const int kOps = 2 * stages + 4, kOffMisc = off_bar + 8 * (2 * stages + 4 + kEpiWarps * kOpSlots);
+  const int kOps = 2 * stages + 4, kDrain = kOps + kEpiWarps * kOpSlots, kOffMisc = off_bar + 8 * (kDrain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 8);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = ptx::cluster_rank();
@@ -520,6 +528,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
       ptx::mbar_init(bar(kAccFree + b), 2 * kEpiWarps);
     }
     for (int i = 0; i < kEpiWarps * kOpSlots; ++i) ptx::mbar_init(bar(kOps + i), 1);
+    ptx::mbar_init(bar(kDrain), 1);
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&tmW);
     ptx::prefetch_tmap(&tmX);
@@ -576,7 +585,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     if (even)
       for (int64_t i = g > stages ? g - stages : 0; i < g; ++i)
         __all_sync(0xffffffffu, ptx::mbar_wait_cluster_timed(bar(kFull + (int)(i % stages)),
-                                                             (uint32_t)((i / stages) & 1), p.timeout_ns));
+                                                             (uint32_t)((i / stages) & 1), drain_ns(p)));
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer (even CTA)
     if (even) {
@@ -610,6 +619,11 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
             parity ^= 1;
           }
         }
+      }
+      // after a wait that ran out: the MMAs issued so far end before the pair's memory goes
+      if (__any_sync(0xffffffffu, *abort_flag != 0)) {
+        if (leader) ptx::umma_commit_pair(bar(kDrain), 1);
+        __all_sync(0xffffffffu, ptx::mbar_wait_cluster_timed(bar(kDrain), 0, drain_ns(p)));
       }
     }
   } else if (warp < 4) {
@@ -739,7 +753,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
       // operands in flight (after a wait that ran out) land before the CTA may exit
       for (; used < fetched; ++used)
         __all_sync(0xffffffffu, ptx::mbar_wait_cluster_timed(op_bar(used % kOpSlots), (uint32_t)((used / kOpSlots) & 1),
-                                                             p.timeout_ns));
+                                                             drain_ns(p)));
     } else {
       for (int i = pair; i < tiles; i += pairs, ++u) {
         const int b = u & 1;
