@@ -40,39 +40,30 @@ template <int CNT>
 struct Operands {
   __nv_bfloat16 m[CNT], r[CNT];
   __device__ __forceinline__ void load(const Params& p, int64_t at, int tokens) {
-    if (p.mul) {
+    if (p.mul) column(m, p.mul + at, p.N, tokens);
+    if (p.res) column(r, p.res + at, p.N, tokens);
+  }
+  static __device__ __forceinline__ void column(__nv_bfloat16 (&v)[CNT], const __nv_bfloat16* q, int32_t N, int tokens) {
+    if (tokens >= CNT) {
 #pragma unroll
-      for (int j = 0; j < CNT; ++j)
-        if (j < tokens) m[j] = p.mul[at + (int64_t)j * p.N];
-    }
-    if (p.res) {
+      for (int j = 0; j < CNT; ++j, q += N) v[j] = *q;
+    } else {
 #pragma unroll
-      for (int j = 0; j < CNT; ++j)
-        if (j < tokens) r[j] = p.res[at + (int64_t)j * p.N];
+      for (int j = 0; j < CNT; ++j, q += N)
+        if (j < tokens) v[j] = *q;
     }
   }
 };
 
-// Every lane's bytes of lanes first .. first + CNT - 1, four to a word.
-template <int WORDS>
-__device__ __forceinline__ void spread_scales(uint32_t mine, int first, uint32_t (&sx)[WORDS]) {
-#pragma unroll
-  for (int k = 0; k < WORDS; ++k) {
-    sx[k] = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) sx[k] |= __shfl_sync(0xffffffffu, mine, first + 4 * k + e) << (8 * e);
-  }
-}
-
-// Epilogue of those tokens for a feature below N; sx: byte j of word j / 4 of the tokens' scale
-// bytes (8-bit operands). Two tokens' results are converted at once, and a whole chunk is stored
+// Epilogue of those tokens for a feature below N; ws, sx: the feature's and the tokens' scales
+// (8-bit operands). Two tokens' results are converted at once, and a whole chunk is stored
 // without a test per token: single conversions and the tests were most of this function's time.
 template <bool F8, int CNT>
 __device__ __forceinline__ void finish_tokens(const Params& p, float (&v)[CNT], const Operands<CNT>& o, int64_t at,
-                                              int tokens, float bias, float ws, const uint32_t (&sx)[CNT / 4]) {
+                                              int tokens, float bias, float ws, const float (&sx)[CNT]) {
   if (F8) {
 #pragma unroll
-    for (int j = 0; j < CNT; ++j) v[j] = v[j] * ws * scale_of((uint8_t)(sx[j / 4] >> (8 * (j % 4))));
+    for (int j = 0; j < CNT; ++j) v[j] = v[j] * ws * sx[j];
   }
 #pragma unroll
   for (int j = 0; j < CNT; ++j) v[j] += bias;
@@ -99,9 +90,8 @@ __device__ __forceinline__ void finish_tokens(const Params& p, float (&v)[CNT], 
   }
 }
 
-// Where N and every pointer allow it (p.octs), the epilogue moves eight neighbouring features
-// of one token at a time, 16 bytes: one thread's mul, residual and out are one access each,
-// and cost a fifth of the instructions of single elements.
+// Where N and every pointer allow it (p.octs), the few-token kernel's epilogue, whose sums lie
+// in shared memory, moves eight neighbouring features of one token at a time, 16 bytes.
 template <bool F8>
 struct OctConstants {   // as they lie in memory: unpacked where they are used
   uint4 bias;
@@ -421,10 +411,11 @@ __global__ void __launch_bounds__(kSplitThreads) linear_split_kernel(const __gri
       const int64_t at = t * p.N + n;
       Operands<kChunk> ops;
       if (n < p.N) ops.load(p, at, left);
-      uint32_t sx[kChunk / 4] = {};
+      float sx[kChunk];
       if (F8) {
-        const uint32_t mine = lane < left ? p.xs[t + lane] : 0;
-        spread_scales(mine, 0, sx);
+        const float mine = lane < left ? scale_of(p.xs[t + lane]) : 0.f;
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j) sx[j] = __shfl_sync(0xffffffffu, mine, j);
       }
       float v[kChunk] = {};
       for (int s = 0; s < slices; ++s)
@@ -445,35 +436,20 @@ __global__ void __launch_bounds__(kSplitThreads) linear_split_kernel(const __gri
 
 // ------------------------------------------------------------------ many tokens: SM pairs
 // p.nt tokens a tile (a multiple of 16, at most 256; two accumulators in TMEM), p.stages
-// stages. Warp 0 loads, warp 1 issues the MMAs (even CTA), warps 4.. run the epilogue (two per
-// 32 TMEM lanes, on alternate chunks of 16 tokens); with p.octs they bring mul and residual
-// into shared memory by TMA, kOpSlots chunks ahead, else warps 2 and 3 fetch them into L2.
-// (Loaded into registers one chunk ahead instead, the operands of a 4096 x 7168 output kept
-// ~8 KiB in flight per SM and took 29 us.)
+// stages. Warp 0 loads, warp 1 issues the MMAs (even CTA), warps 2 and 3 fetch the epilogue's
+// operands into L2, warps 4.. run the epilogue (two per 32 TMEM lanes, on alternate chunks of
+// 16 tokens; a lane's accesses are its feature's, 64 bytes a warp and token, whatever N's
+// alignment). Where K is short the epilogue is what a tile takes: its instructions count.
+// (Turning the sums through shared memory into 16-byte accesses, with the operands brought by
+// TMA, was no faster: 4096 x 7168 x 512 with a residual and a sigmoid 67 against 55 us.)
 constexpr int kEpiWarps = 8, kEpiSets = kEpiWarps / 4;
 constexpr int kPairThreads = 32 * (4 + kEpiWarps);
-constexpr int kOpSlots = 3;
-constexpr int kOpBytes = kChunk * 32 * 2;      // one operand of a warp's chunk: 16 tokens x 32 features
-// behind the ring: per epilogue warp, 16 tokens x 32 features of sums, on their way from the
-// lanes that own a feature to the lanes that own eight (rows of 36 words: no bank conflicts),
-// and its operand slots
-constexpr int kTurnPitch = 36, kTurnBytes = kChunk * kTurnPitch * 4;
-constexpr int kPairBarBytes = 512, kPairSlack = kPairBarBytes + 1024;
-static_assert(8 * (2 * kMaxStages + 5 + kEpiWarps * kOpSlots) + 16 <= kPairBarBytes, "barriers");
-__host__ __device__ constexpr int pair_extra(int ops) { return kEpiWarps * (kTurnBytes + ops * kOpSlots * kOpBytes); }
-__host__ __device__ constexpr int pair_smem(int nt, int stages, int ops) {
-  return stages * stage_bytes_of(nt) + pair_extra(ops) + kPairSlack;
+// behind the ring: per epilogue warp, its tile's token scales (8-bit operands)
+constexpr int kScaleBytes = kEpiWarps * 256 * 4;
+__host__ __device__ constexpr int pair_smem(int nt, int stages) {
+  return stages * stage_bytes_of(nt) + kScaleBytes + kSmemSlack;
 }
-
-// A tile's scale bytes of x, four to a word: byte k of word h is token 128 h + 32 k + lane's.
-__device__ __forceinline__ void load_scales(const Params& p, int64_t t0, int tokens, int lane, uint32_t (&xb)[2]) {
-  uint32_t byte[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) byte[k] = 32 * k + lane < tokens ? p.xs[t0 + 32 * k + lane] : 0;
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-    xb[k] = byte[4 * k] | byte[4 * k + 1] << 8 | byte[4 * k + 2] << 16 | byte[4 * k + 3] << 24;
-}
+static_assert(8 * (2 * kMaxStages + 5) + 16 <= kBarBytes, "barriers");
 
 constexpr int kGroupT = 8;   // token tiles that share a sweep over the feature tiles
 
@@ -491,9 +467,7 @@ __device__ __forceinline__ TileAt tile_of(uint32_t i, uint32_t tiles_n, uint32_t
 
 template <bool F8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
-linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
-                   const __grid_constant__ CUtensorMap tmMul, const __grid_constant__ CUtensorMap tmRes,
-                   const Params p) {
+linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Params p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = ptx::smem_u32(smem);
@@ -501,12 +475,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
   // CTA), accumulator free (even CTA: both CTAs' epilogue warps)
   const int nt = p.nt, stages = p.stages;
   const uint32_t stage_bytes = (uint32_t)stage_bytes_of(nt);
-  const int ops = p.octs ? (p.mul != nullptr) + (p.res != nullptr) : 0;
-  const int off_ops = stages * (int)stage_bytes, off_turn = off_ops + kEpiWarps * ops * kOpSlots * kOpBytes;
-  const int off_bar = stages * (int)stage_bytes + pair_extra(ops);
+  const int off_scale = stages * (int)stage_bytes, off_bar = off_scale + kScaleBytes;
   auto bar = [&](int i) { return sbase + off_bar + 8u * i; };
   const int kFull = 0, kEmpty = stages, kAccFull = 2 * stages, kAccFree = 2 * stages + 2;
-  const int kOps = 2 * stages + 4, kDrain = kOps + kEpiWarps * kOpSlots, kOffMisc = off_bar + 8 * (kDrain + 1);
+  const int kDrain = 2 * stages + 4, kOffMisc = off_bar + 8 * (kDrain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + kOffMisc + 8);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = ptx::cluster_rank();
@@ -527,7 +499,6 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
       ptx::mbar_init(bar(kAccFull + b), 1);
       ptx::mbar_init(bar(kAccFree + b), 2 * kEpiWarps);
     }
-    for (int i = 0; i < kEpiWarps * kOpSlots; ++i) ptx::mbar_init(bar(kOps + i), 1);
     ptx::mbar_init(bar(kDrain), 1);
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&tmW);
@@ -628,7 +599,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     }
   } else if (warp < 4) {
     // ---------------------------------------------------------------- the epilogue's operands into L2
-    if (!p.octs && (p.mul || p.res)) {
+    if (p.mul || p.res) {
       int u = 0;
       for (int i = pair; i < tiles; i += pairs, ++u) {
         // a tile's own main loop is the time to fetch its operands: wait for the one before it
@@ -657,135 +628,49 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive_cluster_relaxed(lead(bar(kAccFree + b)));
     };
+    float* scale = reinterpret_cast<float*>(smem + off_scale) + (warp - 4) * 256;
     int u = 0;
-    if (p.octs) {
-      // lane: features n .. n + 7 of tokens lane / 4 and lane / 4 + 8 of a chunk
-      float* turn = reinterpret_cast<float*>(smem + off_turn + (warp - 4) * kTurnBytes);
-      const int slot_bytes = ops * kOpBytes, off_slots = off_ops + (warp - 4) * kOpSlots * slot_bytes;
-      auto op_bar = [&](int slot) { return bar(kOps + (warp - 4) * kOpSlots + slot); };
-      // the next chunk whose operands are to be fetched
-      Tile ft = tile_at(min(pair, tiles - 1));
-      int fi = pair, fc = kChunk * set, fetched = 0, used = 0;
-      auto fetch = [&]() {
-        while (fi < tiles && (fc >= ft.tokens || ft.nw >= p.N)) {
-          fi += pairs;
-          fc = kChunk * set;
-          if (fi < tiles) ft = tile_at(fi);
-        }
-        if (fi >= tiles) return;
-        if (lane == 0) {
-          const int slot = fetched % kOpSlots;
-          const uint32_t dst = sbase + off_slots + slot * slot_bytes;
-          ptx::mbar_arrive_expect_tx(op_bar(slot), (uint32_t)slot_bytes);
-          if (p.mul) ptx::tma_load_2d(dst, &tmMul, op_bar(slot), ft.nw, (int32_t)ft.t0 + fc);
-          if (p.res) ptx::tma_load_2d(dst + slot_bytes - kOpBytes, &tmRes, op_bar(slot), ft.nw, (int32_t)ft.t0 + fc);
-        }
-        ++fetched;
-        fc += kEpiSets * kChunk;
-      };
-      if (ops > 0)
-        for (int k = 0; k < kOpSlots; ++k) fetch();
-      // a tile's constants, and its tokens' scale bytes (lane: tokens lane, lane + 32, ..), are
-      // loaded a tile ahead
-      OctConstants<F8> constants, constants2;
-      uint32_t xb[2] = {0, 0}, xb2[2] = {0, 0};
-      auto prepare = [&](const Tile& t) {
-        constants2.load(p, t.nw + 8 * (lane % 4));
-        if (F8) load_scales(p, t.t0, t.tokens, lane, xb2);
-      };
-      Tile t = tile_at(min(pair, tiles - 1)), after = t;
-      prepare(t);
-      bool ok = true;
-      for (int i = pair; i < tiles && ok; i += pairs, ++u) {
-        const int b = u & 1;
-        t = after;
-        constants = constants2;
-        xb[0] = xb2[0];
-        xb[1] = xb2[1];
-        if (i + pairs < tiles) {
-          after = tile_at(i + pairs);
-          prepare(after);
-        }
-        const int32_t n = t.nw + 8 * (lane % 4);
-        const uint32_t trow = tbase + ((32u * q) << 16) + b * nt;
-        if (!wait_all(bar(kAccFull + b), (uint32_t)((u >> 1) & 1))) { give_up(); ok = false; break; }
-        ptx::tc_fence_after();
-#pragma unroll 1
-        for (int c = kChunk * set; c < t.tokens; c += kEpiSets * kChunk) {
-          float v[kChunk];
-          ptx::tmem_ld_32x32b_x16(trow + c, v);
-          const int slot = used % kOpSlots;
-          const bool with_ops = ops > 0 && t.nw < p.N;
-          if (with_ops && !wait_all(op_bar(slot), (uint32_t)((used / kOpSlots) & 1))) {
-            ptx::tmem_wait_ld();
-            give_up();
-            ok = false;
-            break;
-          }
-          const uint4* om = reinterpret_cast<const uint4*>(smem + off_slots + slot * slot_bytes) + lane;
-          const uint4* orr = om + (slot_bytes - kOpBytes) / 16;
-          const uint32_t scales = xb[c >= 128] >> (8 * (c / 32 % 4));      // of tokens c / 32 * 32 + lane
-          ptx::tmem_wait_ld();
+    for (int i = pair; i < tiles; i += pairs, ++u) {
+      const int b = u & 1;
+      const Tile t = tile_at(i);
+      const int32_t n = t.nw + lane;
+      const float bias = p.bias && n < p.N ? __bfloat162float(p.bias[n]) : 0.f;
+      const float ws = F8 && n < p.N ? scale_of(p.ws[n]) : 1.f;
+      if (F8) {
+        __syncwarp();      // the tile before is read
 #pragma unroll
-          for (int j = 0; j < kChunk; ++j) turn[j * kTurnPitch + lane] = v[j];
-          __syncwarp();
+        for (int k = 0; k < 8; ++k) {
+          const int j = 32 * k + lane;
+          scale[j] = j < t.tokens ? scale_of(p.xs[t.t0 + j]) : 0.f;
+        }
+        __syncwarp();
+      }
+      const uint32_t trow = tbase + ((32u * q) << 16) + b * nt;
+      const int64_t step = (int64_t)kEpiSets * kChunk * p.N;
+      int c = kChunk * set;
+      int64_t at = (t.t0 + c) * p.N + n;
+      // a chunk's operands are loaded before the chunk before it is finished
+      Operands<kChunk> ops, next;
+      if (c < t.tokens && n < p.N) ops.load(p, at, t.tokens - c);
+      if (!wait_all(bar(kAccFull + b), (uint32_t)((u >> 1) & 1))) { give_up(); break; }
+      ptx::tc_fence_after();
+#pragma unroll 2
+      for (; c < t.tokens; c += kEpiSets * kChunk, at += step) {
+        float v[kChunk];
+        ptx::tmem_ld_32x32b_x16(trow + c, v);
+        const int left = t.tokens - c, then = left - kEpiSets * kChunk;
+        if (then > 0 && n < p.N) next.load(p, at + step, then);
+        float sx[kChunk];
+        if (F8) {
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int j = lane / 4 + 8 * h;
-            const float4* w = reinterpret_cast<const float4*>(turn + j * kTurnPitch + 8 * (lane % 4));
-            const float4 lo = w[0], hi = w[1];
-            float f[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-            uint4 m, r;
-            if (p.mul) m = om[32 * h];
-            if (p.res) r = orr[32 * h];
-            float xs = 1.f;
-            if (F8) xs = scale_of((uint8_t)__shfl_sync(0xffffffffu, scales, c % 32 + j));
-            if (c + j < t.tokens && n < p.N) finish_oct<F8>(p, f, m, r, xs, constants, (t.t0 + c + j) * p.N + n);
-          }
-          __syncwarp();      // the chunk's operands and sums are read
-          if (with_ops) {
-            ++used;
-            fetch();
-          }
+          for (int j = 0; j < kChunk; j += 4) *reinterpret_cast<float4*>(sx + j) = *reinterpret_cast<const float4*>(scale + c + j);
         }
-        release(b);
+        ptx::tmem_wait_ld();
+        if (n < p.N) finish_tokens<F8, kChunk>(p, v, ops, at, left, bias, ws, sx);
+        ops = next;
+        __syncwarp();
       }
-      // operands in flight (after a wait that ran out) land before the CTA may exit
-      for (; used < fetched; ++used)
-        __all_sync(0xffffffffu, ptx::mbar_wait_cluster_timed(op_bar(used % kOpSlots), (uint32_t)((used / kOpSlots) & 1),
-                                                             drain_ns(p)));
-    } else {
-      for (int i = pair; i < tiles; i += pairs, ++u) {
-        const int b = u & 1;
-        const Tile t = tile_at(i);
-        const int32_t n = t.nw + lane;
-        const float bias = p.bias && n < p.N ? __bfloat162float(p.bias[n]) : 0.f;
-        const float ws = F8 && n < p.N ? scale_of(p.ws[n]) : 1.f;
-        uint32_t xb[2] = {0, 0};
-        if (F8) load_scales(p, t.t0, t.tokens, lane, xb);
-        const int64_t at = t.t0 * p.N + n;
-        const uint32_t trow = tbase + ((32u * q) << 16) + b * nt;
-        int c = kChunk * set;
-        Operands<kChunk> ops, next;
-        if (c < t.tokens && n < p.N) ops.load(p, at + (int64_t)c * p.N, t.tokens - c);
-        if (!wait_all(bar(kAccFull + b), (uint32_t)((u >> 1) & 1))) { give_up(); break; }
-        ptx::tc_fence_after();
-#pragma unroll 1
-        for (; c < t.tokens; c += kEpiSets * kChunk) {
-          float v[kChunk];
-          ptx::tmem_ld_32x32b_x16(trow + c, v);
-          const int then = c + kEpiSets * kChunk;
-          if (then < t.tokens && n < p.N) next.load(p, at + (int64_t)then * p.N, t.tokens - then);
-          ptx::tmem_wait_ld();
-          uint32_t sx[kChunk / 4] = {};
-          if (F8) spread_scales(xb[c >= 128] >> (8 * (c / 32 % 4)) & 0xFFu, c % 32, sx);   // of tokens c / 32 * 32 + lane
-          if (n < p.N)
-            finish_tokens<F8, kChunk>(p, v, ops, at + (int64_t)c * p.N, t.tokens - c, bias, ws, sx);
-          ops = next;
-          __syncwarp();
-        }
-        release(b);
-      }
+      release(b);
     }
   }
   __syncthreads();

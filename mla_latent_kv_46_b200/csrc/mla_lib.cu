@@ -1460,19 +1460,12 @@ mla_status launch_linear_pair(const void* x, const void* W, mla::lin::Params p, 
   CUtensorMap tw, tx;
   if (mla_status s = linear_maps<F8>(&tw, &tx, W, x, p, kM, (uint32_t)nt / 2)) return s;
   if (mla_status s = ensure_smem_attr((const void*)kern, kSmemOfOne)) return s;
-  const int ops = p.octs ? (p.mul != nullptr) + (p.res != nullptr) : 0;
-  CUtensorMap tm = tx, tr = tx;
-  if (p.octs && p.mul)
-    if (mla_status s = make_store_map_2d(&tm, p.mul, false, p.N, p.T, (uint64_t)p.N * 2, 32, kChunk)) return s;
-  if (p.octs && p.res)
-    if (mla_status s = make_store_map_2d(&tr, p.res, false, p.N, p.T, (uint64_t)p.N * 2, 32, kChunk)) return s;
   p.nt = nt;
-  p.stages = std::min(kMaxStages, (kSmemOfOne - pair_smem(nt, 0, ops)) / stage_bytes_of(nt));
+  p.stages = std::min(kMaxStages, (kSmemOfOne - pair_smem(nt, 0)) / stage_bytes_of(nt));
   const int64_t tiles = (((int64_t)p.N + 2 * kM - 1) / (2 * kM)) * (((int64_t)p.T + nt - 1) / nt);
   if (tiles > 0x7FFF0000) return fail(MLA_ERR_UNSUPPORTED, "%s: T=%d N=%d is too large", what, p.T, p.N);
   const unsigned pairs = (unsigned)std::min<int64_t>(tiles, std::max(1, sms / 2));
-  return launch_overlapped(what, kern, dim3(2 * pairs), kPairThreads, pair_smem(nt, p.stages, ops), 0, st, tw, tx, tm,
-                           tr, p);
+  return launch_overlapped(what, kern, dim3(2 * pairs), kPairThreads, pair_smem(nt, p.stages), 0, st, tw, tx, p);
 }
 
 // Which kernel, tokens per tile and K slices. Both kernels' times are estimated from the sizes
