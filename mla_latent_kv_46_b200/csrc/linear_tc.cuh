@@ -189,7 +189,7 @@ __host__ __device__ constexpr int split_smem(int nt, int stages, int slices) {
 }
 
 template <bool F8>
-__global__ void __launch_bounds__(kSplitThreads) linear_split_kernel(const __grid_constant__ CUtensorMap tmW,
+__global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __grid_constant__ CUtensorMap tmW,
                                                                      const __grid_constant__ CUtensorMap tmX,
                                                                      const Params p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];

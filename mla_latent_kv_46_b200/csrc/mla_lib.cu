@@ -1471,10 +1471,10 @@ mla_status launch_linear_pair(const void* x, const void* W, mla::lin::Params p, 
 // Which kernel, tokens per tile and K slices. Both kernels' times are estimated from the sizes
 // and the cheapest of a few candidates taken. The constants (microseconds, bytes per
 // microsecond) were fitted to 340 sizes on a B200, T = 1 .. 4096, N = 130 .. 16384, K = 300 ..
-// 16384, both operand types, 3,000 measured variants: the pick is within 1.3 % of the fastest
-// variant on the (geometric) average and 20 % off at worst. What decides, per K block of a CTA:
-// its 16 KiB of W and 64 bytes a token of x through the SM's 105-120 KB/us, or the MMA's 1.2 ns
-// a token; over all CTAs: the operands' bytes from HBM; and behind that the epilogue.
+// 16384, both operand types, 3,000 measured variants: the pick is within 1.6 % of the fastest
+// variant on the (geometric) average and 30 % off at worst. What decides, per K block of a CTA:
+// its 16 KiB of W and 64 bytes a token of x through the SM's 100-107 KB/us, or the MMA's 0.82
+// ns a token; over all CTAs: the operands' bytes from HBM; and behind that the epilogue.
 struct LinearChoice {
   bool pair;      // the persistent kernel
   int nt, slices;
@@ -1485,7 +1485,7 @@ LinearChoice choose_linear(const mla::lin::Params& p, bool f8, int sms) {
   const int64_t tiles_n = ((int64_t)p.N + 2 * kM - 1) / (2 * kM);
   const double bytes = ((double)p.T + p.N) * p.K * (f8 ? 1 : 2) +
                        2.0 * p.T * p.N * (1 + (p.mul != nullptr) + (p.res != nullptr));
-  const double hbm = bytes / 7.7e6, pairs = std::max(1, sms / 2);
+  const double hbm = bytes / 8.0e6, pairs = std::max(1, sms / 2);
   auto up16 = [](int64_t v) { return (int)((v + 15) / 16 * 16); };
   LinearChoice best{true, 256, 1};
   double best_us = 1e30;
@@ -1497,8 +1497,8 @@ LinearChoice choose_linear(const mla::lin::Params& p, bool f8, int sms) {
   };
   auto pair = [&](int nt) {
     const double waves = std::ceil(tiles_n * std::ceil((double)p.T / nt) / pairs);
-    const double block = std::max((kABytes + 64.0 * nt) / 120e3, 1.2e-3 * nt), epilogue = 1.6 + 0.023 * nt;
-    consider({true, nt, 1}, 3.1 + std::max(waves * std::max(kblk * block, epilogue), hbm) + epilogue);
+    const double block = std::max((kABytes + 64.0 * nt) / 107e3, 0.82e-3 * nt), epilogue = 1.94 + 0.0108 * nt;
+    consider({true, nt, 1}, 2.9 + std::max(waves * std::max(kblk * block, epilogue), hbm) + epilogue);
   };
   const int64_t least = ((int64_t)p.T + 255) / 256;      // token tiles of 256
   for (int64_t j = least; j < least + 4; ++j)
@@ -1519,9 +1519,9 @@ LinearChoice choose_linear(const mla::lin::Params& p, bool f8, int sms) {
         if (split_smem(nt, 1, slices) > kSmemOfOne) continue;
         const double waves = std::ceil(tiles / (fit * (two ? 2 : 1)));
         const double share = std::min(two ? 2.0 : 1.0, std::max(1.0, 2 * slices * tiles / sms));   // CTAs at work an SM
-        const double block = std::max({(kABytes + 64.0 * nt) * share / 105e3, 1.2e-3 * nt * share, 0.115});
-        const double tail = 0.9 + (slices > 1 ? 1.4 : 0.0) + 0.0345 * nt / std::min(slices, nt / 16);
-        consider({false, nt, slices}, 8.0 + std::max(waves * std::ceil((double)kblk / slices) * block, hbm) + waves * tail);
+        const double block = std::max({(kABytes + 64.0 * nt) * share / 100e3, 0.82e-3 * nt * share, 0.15});
+        const double tail = 1.1 + (slices > 1 ? 0.65 : 0.0) + 0.026 * nt / std::min(slices, nt / 16);
+        consider({false, nt, slices}, 6.2 + std::max(waves * std::ceil((double)kblk / slices) * block, hbm) + waves * tail);
       }
     }
   return best;
