@@ -18,6 +18,9 @@
  *   mla_decode_attn    scores, online softmax and latent value sum per unit
  *   mla_combine        log-sum-exp merge of units that share a query
  *   mla_out_proj       out = W_UV[h] @ o_lat                          (per head)
+ * and around it, from the residual stream to the residual stream: mla_add_rmsnorm,
+ * mla_linear (queries), mla_cache_write in the place of the append, and mla_linear for the
+ * output gate and Wo.
  *
  * Conventions for every call:
  *  - Tensor pointers are DEVICE pointers unless the name ends in _host; all
@@ -79,9 +82,10 @@ typedef struct {
   int32_t dtype;      /* mla_dtype */
 } mla_dims;
 
-/* Kernel selection for mla_decode_attn / mla_absorb_q / mla_out_proj.
+/* Kernel selection for mla_decode_attn / mla_absorb_q / mla_out_proj / mla_linear(_fp8).
  * AUTO: tensor-core (tcgen05) kernels where the dims allow (bf16, R=512, Dr=64,
- * page_size=64, H a multiple of 64, Dn=Dv=128), else the SIMT CUDA kernels.
+ * page_size=64, H a multiple of 64, Dn=Dv=128; mla_linear: x and W 16-byte aligned with
+ * rows of a multiple of 16 bytes), else the SIMT CUDA kernels.
  * SIMT: always the SIMT CUDA kernels. TCGEN05: tensor-core kernels or
  * MLA_ERR_UNSUPPORTED. There is no CPU path. */
 typedef enum { MLA_POLICY_AUTO = 0, MLA_POLICY_SIMT = 1, MLA_POLICY_TCGEN05 = 2 } mla_policy;
@@ -241,8 +245,8 @@ mla_status mla_combine(const int32_t* plan_dev, const mla_plan_info* info, const
 
 /* ---------------------------------------------------------------- a7: output up-projection
  * out[t][h][:] = W_UV[h] @ o_lat[t][h][:]  (the value up-projection folded into
- * the output side; GatedMLA "Output projection and optional gate" applies Wo and
- * the gate after this, outside this library).
+ * the output side; GatedMLA "Output projection and optional gate" applies the gate and
+ * Wo after this: mla_linear).
  *   o_lat [T][H][R] fp32, W_UV [H][Dv][R] dtype  ->  out [T][H][Dv] dtype
  * (bf16 on the tensor cores: each fp32 o_lat element enters as bf16 hi + lo, two MMAs
  * per K step, so o_lat keeps ~16 significant bits; fp32 accumulation)              */
@@ -305,7 +309,7 @@ mla_status mla_decode_attn_fp8(const void* q_lat, const void* q_rope, const void
  * scale = 1/sqrt(Dn + Dr) as for the decode. The non-absorbed form is the cheaper one when
  * every position is a query: 2 (Dn + Dr + Dv) FLOP per head and (query, key) pair against
  * the absorbed form's 2 (R + Dr + R). The output gate and Wo that follow in GatedMLA are
- * plain projections outside this library.
+ * mla_linear (below).
  *   ckr        [N][R+Dr] bf16: the packed sequences' rows [c ; k_rope] (k_rope rotated)
  *   q_nope     [N][H][Dn], q_rope [N][H][Dr] bf16 (q_rope rotated)
  *   W_UK [H][Dn][R], W_UV [H][Dv][R] bf16
@@ -361,7 +365,11 @@ mla_status mla_quantize_fp8(const void* rows, void* codes, void* scales, int32_t
  * normal distribution function Phi (the erf form). */
 typedef enum { MLA_ACT_NONE = 0, MLA_ACT_SIGMOID = 1, MLA_ACT_SILU = 2, MLA_ACT_GELU = 3 } mla_act;
 
-/* out[t][n] = residual[t][n] + mul[t][n] * act(sum_k x[t][k] W[n][k] + bias[n])
+/* Tensor cores: rows of x and W of a multiple of 16 bytes, both 16-byte aligned (K a multiple of
+ * 8 in bf16, of 16 in 8 bits); any other size or alignment runs on CUDA cores, far slower.
+ * Sums in a fixed order: two calls with the same arguments give the same bits.
+ *
+ * out[t][n] = residual[t][n] + mul[t][n] * act(sum_k x[t][k] W[n][k] + bias[n])
  *   x [T][K], W [N][K] (out x in, as W_DKV), bias [N], mul [T][N], residual [T][N],
  *   out [T][N]: bf16. bias, mul and residual may each be NULL (0, 1 and 0).
  * mul serves the output gate (sigmoid(x Wg^T) * attention) and a gated feed-forward's
