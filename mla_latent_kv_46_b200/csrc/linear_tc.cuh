@@ -2,22 +2,27 @@
 //
 //   out[t][n] = residual + mul * act(sum_k x[t][k] W[n][k] + bias[n])
 //
-// Both kernels compute the transposed product D[n][t]: W's rows are the MMA's M side (128
-// a CTA), the tokens its N side. One token then still fills the M side, so a decode step's
+// Both kernels compute the transposed product D[n][t]: W's rows are the MMA's M side, the
+// tokens its N side. One token then still fills the M side, so a decode step's
 // few tokens cost no idle rows, only the 16-token minimum of the N side; and a thread of the
 // epilogue owns one feature (its TMEM lane), so a warp's store of one token covers 32
 // neighbouring features. x and W are both K-major: TMA streams 128-byte-wide K blocks (64
 // bf16 or 128 E4M3 elements, 128-byte swizzle) and one elected lane issues the MMAs, fp32 in
 // TMEM. Rows and columns past T, N and K arrive as zeros and are not stored.
 //
-// linear_split_kernel (few tokens): bound by the bytes of W. One CTA per 128 features x NT
-// tokens x K slice; the slices of a tile are a cluster, which adds its fp32 partial sums
-// through distributed shared memory in slice order. One launch, no workspace, and the same
-// sum in every run.
+// Both run on pairs of CTAs (tcgen05 cta_group::2): 256 features x nt tokens a tile, each CTA
+// loading its 128 rows of W and half of the tokens' rows of x, which halves what an SM takes in
+// of x. nt is chosen per call.
 //
-// linear_pair_kernel (many tokens): bound by the tensor cores. Persistent pairs of CTAs
-// (tcgen05 cta_group::2), 256 features x NT tokens a tile, with two accumulators in TMEM so
-// that a tile's epilogue runs under the next tile's main loop.
+// linear_split_kernel (few tokens): bound by the bytes of W. One pair per tile and K slice; the
+// slices of a tile are a cluster, which adds its fp32 partial sums through distributed shared
+// memory in slice order. One launch, no workspace, and the same sum in every run. (128 x 7168 x
+// 16384 bf16: 45 us against 36 for W's bytes; 8 bits: 28 against 18. One token, 16384 x 7168: 38.5
+// and 21.7.)
+//
+// linear_pair_kernel (many tokens): bound by the tensor cores. Persistent pairs, with two
+// accumulators in TMEM so that a tile's epilogue runs under the next tile's main loop (16384 x
+// 8192 x 7168 bf16: 1.24 ms, 1.56 PFLOP/s, in a short run; 1.48 ms under the power cap).
 #pragma once
 
 #include "common.cuh"
@@ -155,7 +160,18 @@ __device__ __forceinline__ void prefetch_rows(const Params& p, int64_t t0, int c
 constexpr int kMaxStages = 12;
 // How long a kernel that gave up waits for its own copies and MMAs in flight, which land
 // within microseconds, however short the caller's bound on waits is.
-__device__ __forceinline__ uint64_t drain_ns(const Params& p) { return p.timeout_ns > 10000000ull ? p.timeout_ns : 10000000ull; }
+__device__ __forceinline__ uint64_t drain_ns(const Params& p) {
+  return p.timeout_ns > 10000000ull ? p.timeout_ns : 10000000ull;
+}
+constexpr uint64_t kSettleNs = 100000;
+// The even CTA's loader: the last `stages` armed phases of the full barriers complete (both
+// CTAs' loads), or, if the peer gave up before its share, time out once.
+template <class Bar>
+__device__ __forceinline__ void drain_loads(int64_t armed, int stages, const Bar& full, uint64_t ns) {
+  for (int64_t i = armed > stages ? armed - stages : 0; i < armed; ++i)
+    if (!__all_sync(0xffffffffu, ptx::mbar_wait_cluster_timed(full((int)(i % stages)), (uint32_t)((i / stages) & 1), ns)))
+      break;
+}
 constexpr int kBarBytes = 256;       // barriers and two words behind the ring
 constexpr int kSmemSlack = kBarBytes + 1024;
 static_assert(8 * (2 * kMaxStages + 4) + 16 <= kBarBytes, "barriers");
@@ -169,12 +185,12 @@ __host__ __device__ constexpr uint32_t tmem_cols(int cols) {
 
 // ------------------------------------------------------------------ few tokens: K slices
 // grid (2 slices, feature tiles, token tiles), clusters of 2 slices CTAs: pair after pair.
-// Warp 0 loads, warp 1 of the even CTA issues the MMAs, warps 3.. fetch the epilogue's operands into L2 meanwhile, and all warps
-// run the epilogue. p.nt tokens a tile (a multiple of 16, at most 256), p.stages stages.
+// Warp 0 loads, warp 1 of the even CTA issues the MMAs, warps 3.. fetch the epilogue's
+// operands into L2 meanwhile, and all warps run the epilogue. p.nt tokens a tile (a multiple of 16, at most 256), p.stages stages.
 constexpr int kSplitThreads = 256;
 __host__ __device__ constexpr int stage_bytes_of(int nt) { return kABytes + nt / 2 * kKBytes; }
 // the ring, and in the same place the slices' sums of the CTA's own tokens (chunks of
-// kChunk tokens are dealt to the CTAs of a cluster in turn)
+// kChunk tokens are dealt to the pairs of a cluster in turn)
 constexpr int kChunk = 16;
 __host__ __device__ constexpr int split_chunk_slots(int nt, int slices) {
   return slices * ((nt / kChunk + slices - 1) / slices);
@@ -203,7 +219,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
   const int off_bar = split_ring(nt, stages, slices);
   // barriers: full (even CTA: both CTAs' loads), empty and done (each CTA), drain (even CTA)
   auto bar = [&](int i) { return sbase + off_bar + 8u * i; };
-  const int kFull = 0, kEmpty = stages, kDone = 2 * stages, kDrain = 2 * stages + 1, off_misc = off_bar + 8 * (2 * stages + 2);
+  const int kFull = 0, kEmpty = stages, kDone = 2 * stages, kDrain = 2 * stages + 1;
+  const int off_misc = off_bar + 8 * (2 * stages + 2);
   auto lead = [&](uint32_t a) { return ptx::map_peer(a, 2 * slice); };
   const uint16_t both = (uint16_t)(3u << (2 * slice));
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + off_misc + 8);
@@ -273,9 +290,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
       }
     }
     // the loads in flight land before the pair may exit (both CTAs' count on these barriers)
-    if (even)
-      for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
-        __all_sync(0xffffffffu, ptx::mbar_wait_cluster_timed(bar(kFull + i % stages), (i / stages) & 1, drain_ns(p)));
+    if (even) drain_loads(issued, stages, [&](int s) { return bar(kFull + s); }, drain_ns(p));
+    if (!ok) ptx::delay_ns(kSettleNs);
   } else if (warp == 1 && even) {
     // ---------------------------------------------------------------- MMA issuer
     const bool leader = ptx::elect_one();
@@ -328,8 +344,8 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
   const bool done = ok && wait_all(bar(kDone), 0);
   if (!done) give_up();
   ptx::tc_fence_after();
-  // Chunk c of the tokens is finished by CTA c % slices: every CTA stores its sums straight
-  // from TMEM into that CTA's shared memory, [slice][c / slices][token][feature]. Remote
+  // Chunk c of the tokens is finished by pair c % slices: every CTA stores its sums straight
+  // from TMEM into the shared memory of that pair's CTA for the same features, [slice][c / slices][token][feature]. Remote
   // stores need no answer; reading the peers' sums instead, a round trip per four tokens,
   // took ~10 us more at T = 128 (five slices). The stages they land in are free once every
   // CTA of the cluster has passed its done barrier.
@@ -436,12 +452,11 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
 
 // ------------------------------------------------------------------ many tokens: SM pairs
 // p.nt tokens a tile (a multiple of 16, at most 256; two accumulators in TMEM), p.stages
-// stages. Warp 0 loads, warp 1 issues the MMAs (even CTA), warps 2 and 3 fetch the epilogue's
-// operands into L2, warps 4.. run the epilogue (two per 32 TMEM lanes, on alternate chunks of
-// 16 tokens; a lane's accesses are its feature's, 64 bytes a warp and token, whatever N's
+// stages. Warp 0 loads, warp 1 issues the MMAs (even CTA), warp 2 holds TMEM, warps 4.. run the
+// epilogue (two per 32 TMEM lanes, on alternate chunks of 16 tokens; a lane's accesses are its feature's, 64 bytes a warp and token, whatever N's
 // alignment). Where K is short the epilogue is what a tile takes: its instructions count.
 // (Turning the sums through shared memory into 16-byte accesses, with the operands brought by
-// TMA, was no faster: 4096 x 7168 x 512 with a residual and a sigmoid 67 against 55 us.)
+// TMA, was no faster: 4096 x 7168 x 512 with a residual and a sigmoid 67 against 58 us.)
 constexpr int kEpiWarps = 8, kEpiSets = kEpiWarps / 4;
 constexpr int kPairThreads = 32 * (4 + kEpiWarps);
 // behind the ring: per epilogue warp, its tile's token scales (8-bit operands)
@@ -553,10 +568,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
       }
     }
     // the loads in flight land before the pair may exit (both CTAs' count on these barriers)
-    if (even)
-      for (int64_t i = g > stages ? g - stages : 0; i < g; ++i)
-        __all_sync(0xffffffffu, ptx::mbar_wait_cluster_timed(bar(kFull + (int)(i % stages)),
-                                                             (uint32_t)((i / stages) & 1), drain_ns(p)));
+    if (even) drain_loads(g, stages, [&](int s) { return bar(kFull + s); }, drain_ns(p));
+    if (!ok) ptx::delay_ns(kSettleNs);
   } else if (warp == 1) {
     // ---------------------------------------------------------------- MMA issuer (even CTA)
     if (even) {
@@ -597,19 +610,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         __all_sync(0xffffffffu, ptx::mbar_wait_cluster_timed(bar(kDrain), 0, drain_ns(p)));
       }
     }
-  } else if (warp < 4) {
-    // ---------------------------------------------------------------- the epilogue's operands into L2
-    if (p.mul || p.res) {
-      int u = 0;
-      for (int i = pair; i < tiles; i += pairs, ++u) {
-        // a tile's own main loop is the time to fetch its operands: wait for the one before it
-        if (u > 0 && !wait_all(bar(kAccFull + ((u - 1) & 1)), (uint32_t)(((u - 1) >> 1) & 1))) break;
-        const TileAt at = tile_of(i, tiles_n, tiles_t);
-        const int64_t t0 = (int64_t)at.tt * nt;
-        prefetch_rows(p, t0, (int)min((int64_t)nt, p.T - t0), at.tn * 2 * kM + kM * (int)rank, kM, warp - 2, 2, lane);
-      }
-    }
-  } else {
+  } else if (warp >= 4) {
     // ---------------------------------------------------------------- epilogue
     const int q = warp % 4, set = (warp - 4) / 4;          // TMEM lanes 32q ..; every kEpiSets-th chunk
     struct Tile {
@@ -628,11 +629,18 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive_cluster_relaxed(lead(bar(kAccFree + b)));
     };
+    // this warp's share of a tile's operands into L2, a tile ahead
+    auto prefetch = [&](const Tile& t) {
+      if (p.mul || p.res) prefetch_rows(p, t.t0, t.tokens, t.nw, 32, set, kEpiSets, lane);
+    };
     float* scale = reinterpret_cast<float*>(smem + off_scale) + (warp - 4) * 256;
     int u = 0;
+    Tile t = tile_at(min(pair, tiles - 1)), after = t;
+    prefetch(t);
     for (int i = pair; i < tiles; i += pairs, ++u) {
       const int b = u & 1;
-      const Tile t = tile_at(i);
+      t = after;
+      if (i + pairs < tiles) after = tile_at(i + pairs);
       const int32_t n = t.nw + lane;
       const float bias = p.bias && n < p.N ? __bfloat162float(p.bias[n]) : 0.f;
       const float ws = F8 && n < p.N ? scale_of(p.ws[n]) : 1.f;
@@ -654,6 +662,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
       if (c < t.tokens && n < p.N) ops.load(p, at, t.tokens - c);
       if (!wait_all(bar(kAccFull + b), (uint32_t)((u >> 1) & 1))) { give_up(); break; }
       ptx::tc_fence_after();
+      if (i + pairs < tiles) prefetch(after);      // its main loop is beginning
 #pragma unroll 2
       for (; c < t.tokens; c += kEpiSets * kChunk, at += step) {
         float v[kChunk];
@@ -663,7 +672,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         float sx[kChunk];
         if (F8) {
 #pragma unroll
-          for (int j = 0; j < kChunk; j += 4) *reinterpret_cast<float4*>(sx + j) = *reinterpret_cast<const float4*>(scale + c + j);
+          for (int j = 0; j < kChunk; j += 4)
+            *reinterpret_cast<float4*>(sx + j) = *reinterpret_cast<const float4*>(scale + c + j);
         }
         ptx::tmem_wait_ld();
         if (n < p.N) finish_tokens<F8, kChunk>(p, v, ops, at, left, bias, ws, sx);

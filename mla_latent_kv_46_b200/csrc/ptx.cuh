@@ -61,6 +61,14 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
   }
 }
 
+// Lets `ns` pass (failure paths only: copies whose completion nobody counts any more land
+// within microseconds).
+__device__ __forceinline__ void delay_ns(uint64_t ns) {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < ns) {
+  }
+}
+
 // ------------------------------------------------------------------ TMA
 // 2D tiled load global -> shared, completion counted on an mbarrier (bytes).
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
