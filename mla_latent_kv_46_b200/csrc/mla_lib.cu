@@ -1282,17 +1282,22 @@ int blocks_per_sm(const void* kernel, int threads, int64_t smem) {
     int threads, dev, blocks;
     int64_t smem;
   };
+  constexpr int kKept = 64;
   static std::mutex mu;
-  static std::vector<Known> known;
+  static Known known[kKept];
+  static int kept = 0, next = 0;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
   std::lock_guard<std::mutex> lk(mu);
-  for (const Known& k : known)
+  for (int i = 0; i < kept; ++i) {
+    const Known& k = known[i];
     if (k.kernel == kernel && k.threads == threads && k.smem == smem && k.dev == dev) return k.blocks;
+  }
   int blocks = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, threads, (size_t)smem) != cudaSuccess) blocks = 0;
-  if (known.size() >= 64) known.erase(known.begin());
-  known.push_back({kernel, threads, dev, blocks, smem});
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, threads, (size_t)smem) != cudaSuccess) return 0;
+  known[next] = Known{kernel, threads, dev, blocks, smem};
+  next = (next + 1) % kKept;
+  kept = std::max(kept, next == 0 ? kKept : next);
   return blocks;
 }
 

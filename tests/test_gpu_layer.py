@@ -113,7 +113,7 @@ def run_norm(x, r, gain, T, M, dtype, codes, with_y=True, shift=0, eps=1e-6):
     return t(ro), t(y), t(c), t(s)
 
 
-NORM_SHAPES = [(1, 1), (3, 2), (2, 8), (5, 31), (1, 64), (7, 96), (33, 255), (9, 256), (5, 257), (4, 512), (3, 1000),
+NORM_SHAPES = [(1, 1), (17, 1), (9, 3), (40, 5), (3, 2), (2, 8), (5, 31), (1, 64), (7, 96), (33, 255), (9, 256), (5, 257), (4, 512), (3, 1000),
                (2, 1111), (129, 1536), (2, 4100), (1, 7168), (150, 7168), (2, 8192), (2, 8200), (3, 12290), (1, 16384),
                (2, 16385), (1, 20000), (1, 40001),
                # many rows: the streaming kernel, with rows that are not a multiple of 16 bytes too
