@@ -198,6 +198,12 @@ __device__ __forceinline__ bool mbar_wait_cluster_timed(uint32_t bar, uint32_t p
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The two halves of cluster_sync: what precedes the arrival in any thread of the cluster is
+// visible after the wait in every thread.
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // Bulk copy of `bytes` (multiple of 16, both addresses 16-byte aligned) from this CTA's
 // shared memory into another CTA's of the cluster; completion is signalled to the
 // destination CTA's mbarrier as transaction bytes.
