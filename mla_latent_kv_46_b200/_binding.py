@@ -112,11 +112,23 @@ def _ptr(x):
     return x.data_ptr()
 
 
+_cuda = None   # torch._C once a call needed it: (current device, its current stream's handle)
+
+
+def _cuda_calls():
+    """torch's current-device and current-stream lookups without their Python wrappers (a call's
+    host time is a few microseconds: a Stream object alone takes 3, a repeated import 0.1)."""
+    global _cuda
+    import torch
+    torch.cuda.current_device()      # initialises CUDA
+    _cuda = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+    return _cuda
+
+
 def _stream(s):
     if s is None:
-        import torch
-        # the current stream's handle without a Stream object (0.2 instead of 3 us a call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        device, stream = _cuda or _cuda_calls()
+        return stream(device())
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -266,19 +278,18 @@ def _dense(*tensors):
     """data_ptr of contiguous CUDA tensors on the current device (None -> NULL, integers are
     raw addresses). The calls take row-major buffers of the device they launch on, so a
     strided view, a host tensor or another device's is refused, not misread."""
-    out, device = [], None
+    out, current = [], None
     for x in tensors:
         if x is not None and type(x) is not int:
-            if not x.is_contiguous():
-                raise MlaError(MLA_ERR_INVALID, "argument", "tensor is not contiguous")
-            d = x.get_device()
-            if d != device:
-                if d < 0:
+            device = x.get_device()
+            if device != current or not x.is_contiguous():
+                if not x.is_contiguous():
+                    raise MlaError(MLA_ERR_INVALID, "argument", "tensor is not contiguous")
+                if device < 0:
                     raise MlaError(MLA_ERR_INVALID, "argument", "tensor is not on a CUDA device")
-                import torch
-                if d != torch.cuda.current_device():
-                    raise MlaError(MLA_ERR_INVALID, "argument", f"tensor is on device {d}, not the current one")
-                device = d
+                current = (_cuda or _cuda_calls())[0]()
+                if device != current:
+                    raise MlaError(MLA_ERR_INVALID, "argument", f"tensor is on device {device}, not the current one")
             x = x.data_ptr()
         out.append(x)
     return out

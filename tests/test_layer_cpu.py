@@ -170,3 +170,15 @@ def test_a_host_tensor_is_refused():
         with pytest.raises(mla.MlaError) as e:
             fn(**args)
         assert e.value.status == INVALID
+
+
+@pytest.mark.parametrize("fn,args", [(mla.mla_linear, lin_args(K=33)), (mla.mla_linear, lin_args(x=(1 << 20) + 2)),
+                                     (mla.mla_linear_fp8, lin8_args(K=40)),
+                                     (mla.mla_linear_fp8, lin8_args(W_codes=(2 << 20) + 8))],
+                         ids=["K", "x", "K8", "W8"])
+def test_linear_tensor_core_policy_refuses_what_tma_cannot_move(fn, args):
+    mla.mla_set_policy(mla.MLA_POLICY_TCGEN05)
+    try:
+        refused(fn, args, UNSUPPORTED)
+    finally:
+        mla.mla_set_policy(mla.MLA_POLICY_AUTO)
