@@ -37,9 +37,11 @@ __device__ __forceinline__ float scale_of(uint8_t b) { return __uint_as_float((u
 // negative that e^-v overflows give 0, as the formulas do.
 __device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
 __device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + __expf(-v)); }
-__device__ __noinline__ float gelu(float v) { return 0.5f * v * erfcf(-0.70710678118654752f * v); }
+__device__ __forceinline__ float gelu(float v) { return 0.5f * v * erfcf(-0.70710678118654752f * v); }
+__device__ __noinline__ float4 gelu4(float4 v) { return make_float4(gelu(v.x), gelu(v.y), gelu(v.z), gelu(v.w)); }
 // All of a thread's elements: one branch, straight code behind it (a branch per element of an
-// unrolled epilogue ran out of the instruction cache, as did gelu inlined for each).
+// unrolled epilogue ran out of the instruction cache, as did gelu inlined for each; called for
+// four at a time, whose steps overlap).
 template <int CNT>
 __device__ __forceinline__ void activate(float (&v)[CNT], int act) {
   if (act == kActSigmoid) {
@@ -49,8 +51,19 @@ __device__ __forceinline__ void activate(float (&v)[CNT], int act) {
 #pragma unroll
     for (int j = 0; j < CNT; ++j) v[j] = silu(v[j]);
   } else if (act == kActGelu) {
+    if constexpr (CNT % 4 == 0) {
 #pragma unroll
-    for (int j = 0; j < CNT; ++j) v[j] = gelu(v[j]);
+      for (int j = 0; j < CNT; j += 4) {
+        const float4 g = gelu4(make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]));
+        v[j] = g.x;
+        v[j + 1] = g.y;
+        v[j + 2] = g.z;
+        v[j + 3] = g.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < CNT; ++j) v[j] = gelu(v[j]);
+    }
   }
 }
 
