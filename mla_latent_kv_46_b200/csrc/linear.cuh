@@ -10,6 +10,7 @@
 
 #include "common.cuh"
 #include "fp8_kernels.cuh"
+#include "ptx.cuh"
 
 namespace mla {
 namespace lin {
@@ -37,11 +38,32 @@ __device__ __forceinline__ float scale_of(uint8_t b) { return __uint_as_float((u
 // negative that e^-v overflows give 0, as the formulas do.
 __device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
 __device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + __expf(-v)); }
-__device__ __forceinline__ float gelu(float v) { return 0.5f * v * erfcf(-0.70710678118654752f * v); }
-__device__ __noinline__ float4 gelu4(float4 v) { return make_float4(gelu(v.x), gelu(v.y), gelu(v.z), gelu(v.w)); }
+// v Phi(v). The lower tail Q(x) = Phi(-x) = e^(-x^2 / 2) R(x) for x = |v|, where R falls smoothly
+// from 1/2 to 0 (like 0.4 / x): a polynomial in t = 1 / (1 + 0.35 x) without a constant term,
+// fitted here to R by weighted least squares on x <= 14 (relative error 3.2e-8; above 13.2 the
+// exponential is 0 in fp32). The exponent's roundings (x^2, and its product with log2(e) / 2)
+// are carried to first order, or they would be 1e-5 of the tail. All in all 1e-6 of the result;
+// erfcf took twice the time of a 4685 x 2802 output's whole epilogue.
+__device__ __forceinline__ float gelu(float v) {
+  const float x = fminf(fabsf(v), 20.f);      // above, Q is 0 as well; keeps x^2 finite
+  const float t = __fdividef(1.f, fmaf(0.35f, x, 1.f));
+  float r = -0.029146350920200348f;
+  r = fmaf(r, t, 0.143973708152771f);
+  r = fmaf(r, t, -0.25571832060813904f);
+  r = fmaf(r, t, 0.1591787040233612f);
+  r = fmaf(r, t, -0.02311287634074688f);
+  r = fmaf(r, t, 0.10550924390554428f);
+  r = fmaf(r, t, 0.11983256787061691f);
+  r = fmaf(r, t, 0.13986191153526306f);
+  r = fmaf(r, t, 0.13962140679359436f);
+  const float c = 0.72134752f, c_lo = 9.629815167500055e-09f;
+  const float s = x * x, s_lo = fmaf(x, x, -s);
+  const float y = s * c, y_lo = fmaf(s, c_lo, fmaf(s, c, -y));
+  const float q = ptx::ex2(-y) * (r * t) * fmaf(-0.5f, s_lo, fmaf(-0.69314718f, y_lo, 1.f));
+  return v * (v > 0.f ? 1.f - q : q);
+}
 // All of a thread's elements: one branch, straight code behind it (a branch per element of an
-// unrolled epilogue ran out of the instruction cache, as did gelu inlined for each; called for
-// four at a time, whose steps overlap).
+// unrolled epilogue ran out of the instruction cache).
 template <int CNT>
 __device__ __forceinline__ void activate(float (&v)[CNT], int act) {
   if (act == kActSigmoid) {
@@ -51,19 +73,8 @@ __device__ __forceinline__ void activate(float (&v)[CNT], int act) {
 #pragma unroll
     for (int j = 0; j < CNT; ++j) v[j] = silu(v[j]);
   } else if (act == kActGelu) {
-    if constexpr (CNT % 4 == 0) {
 #pragma unroll
-      for (int j = 0; j < CNT; j += 4) {
-        const float4 g = gelu4(make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]));
-        v[j] = g.x;
-        v[j + 1] = g.y;
-        v[j + 2] = g.z;
-        v[j + 3] = g.w;
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < CNT; ++j) v[j] = gelu(v[j]);
-    }
+    for (int j = 0; j < CNT; ++j) v[j] = gelu(v[j]);
   }
 }
 

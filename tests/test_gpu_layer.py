@@ -392,6 +392,26 @@ def test_linear_activations_at_their_ends(act, lo, hi):
     assert np.all(got[0] == lo) and np.all(np.abs(got[1] - (1.0 if act == "sigmoid" else v)) <= 2.0 ** -8 * v)
 
 
+@pytest.mark.parametrize("T", [100, 0], ids=["few", "all"])
+@pytest.mark.parametrize("act", ["sigmoid", "silu", "gelu"])
+def test_linear_activations_over_their_range(act, T):
+    """Every bf16 value of magnitude 2^-10 .. 20 as a sum by itself: the activation's own error. The
+    exponential's argument is off by at most 2^-24 of its size (20), its approximation and the
+    quotient's by 2^-22: below 2^-18 together, on top of the store's half step."""
+    bits = np.arange(0x3A80, 0x41A1, dtype=np.uint16)
+    v = wl.bf16_bits_to_f32(np.concatenate([bits, bits | 0x8000])).astype(np.float64)
+    v = v[::len(v) // T][:T] if T else v
+    x = np.zeros((len(v), 16))
+    x[:, 3] = v
+    W = np.zeros((8, 16))
+    W[:, 3] = 1
+    got = host(run_linear(bf16(x), bf16(W), None, None, None, len(v), 8, 16, act))
+    ref = layer.activation(v, act)[:, None]
+    # half a step of the binade the value lies in
+    half = np.ldexp(1.0, np.frexp(np.abs(ref))[1] - 9)
+    assert np.all(np.abs(got - ref) <= half * (1 + 2.0 ** -8) + 2.0 ** -18 * np.abs(ref) + 1e-38)
+
+
 def test_two_runs_are_bitwise_equal():
     rng = np.random.default_rng(8)
     for T, N, K in ((1, 7168, 2048), (37, 2000, 4096), (700, 1111, 1000)):
