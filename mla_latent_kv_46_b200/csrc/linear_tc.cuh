@@ -17,12 +17,12 @@
 // linear_split_kernel (few tokens): bound by the bytes of W. One pair per tile and K slice; the
 // slices of a tile are a cluster, which adds its fp32 partial sums through distributed shared
 // memory in slice order. One launch, no workspace, and the same sum in every run. (128 x 7168 x
-// 16384 bf16: 45 us against 36 for W's bytes; 8 bits: 28 against 18. One token, 16384 x 7168: 38.5
-// and 21.7.)
+// 16384 bf16: 45 us against 36 for W's bytes; 8 bits: 27 against 18. One token, 16384 x 7168: 37.6
+// and 21.4.)
 //
 // linear_pair_kernel (many tokens): bound by the tensor cores. Persistent pairs, with two
 // accumulators in TMEM so that a tile's epilogue runs under the next tile's main loop (16384 x
-// 8192 x 7168 bf16: 1.24 ms, 1.56 PFLOP/s, in a short run; 1.48 ms under the power cap).
+// 8192 x 7168 bf16: 1.24 ms, 1.56 PFLOP/s, in a short run; 1.45 ms under the power cap).
 #pragma once
 
 #include "common.cuh"
