@@ -160,8 +160,9 @@ class LayerStep:
     `weights` (torch tensors on the step's device, bf16): gain [M], W_QN [H*Dn, M], W_QR
     [H*Dr, M], W_DKV [R+Dr, M], kv_gain [R], W_O [M, H*Dv] and, for a gated layer, W_G
     [H*Dv, M] (each out x in). projections="fp8": the query, gate and output projections
-    run in 8 bits, their weights quantised here once; the cache write keeps bf16 rows.
-    The step's cache must be the bf16 one (the prologue writes bf16 rows)."""
+    run in 8 bits, their weights quantised here once (finished on return, so that any stream
+    may run the step); the cache write keeps bf16 rows. The step's tensors and its cache must be
+    bf16. One run of an object at a time: its buffers are the step's."""
 
     def __init__(self, step: DecodeStep, weights: dict, projections: str = "bf16", eps: float = 1e-6,
                  rope_base: float = 10000.0):
@@ -170,6 +171,8 @@ class LayerStep:
         if projections not in ("bf16", "fp8"):
             raise ValueError(f"unknown projections {projections!r}")
         spec = step.spec
+        if step.q_nope.dtype != torch.bfloat16:
+            raise ValueError(f"LayerStep needs a bf16 step, not {step.q_nope.dtype}")
         self.step = step
         self.w = weights
         self.fp8 = projections == "fp8"
@@ -179,6 +182,15 @@ class LayerStep:
         self.n_nope, self.n_rope = spec.H * spec.Dn, spec.H * spec.Dr
         self.gated = weights.get("W_G") is not None
         d = step.device
+        # the calls take addresses: a weight of another shape, type or layout would be misread
+        shapes = {"gain": (self.M,), "W_QN": (self.n_nope, self.M), "W_QR": (self.n_rope, self.M),
+                  "W_DKV": (spec.R + spec.Dr, self.M), "kv_gain": (spec.R,), "W_O": (self.M, self.n_out)}
+        if self.gated:
+            shapes["W_G"] = (self.n_out, self.M)
+        for name, shape in shapes.items():
+            if name not in weights:
+                raise ValueError(f"LayerStep needs the weight {name}")
+            self._expect(weights[name], shape, name)
 
         def empty(*shape, dtype=torch.bfloat16):
             return torch.empty(shape, dtype=dtype, device=d)
@@ -197,6 +209,15 @@ class LayerStep:
                 c, s = empty(n, k, dtype=torch.uint8), empty(n, dtype=torch.uint8)
                 mla.mla_quantize_fp8(weights[name], c, s, n, k, mla.MLA_BF16)
                 self.w8[name] = (c, s)
+            torch.cuda.current_stream(d).synchronize()
+
+    def _expect(self, x, shape, name):
+        device = self.step.q_nope.device
+        if tuple(x.shape) != shape or x.dtype != torch.bfloat16 or x.device != device:
+            raise ValueError(f"{name} must be bf16 {list(shape)} on {device}, "
+                             f"got {x.dtype} {list(x.shape)} on {x.device}")
+        if not x.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
 
     def _project(self, name, out, n, act=mla.MLA_ACT_NONE, mul=None, stream=None):
         """out = mul * act(hidden W^T)."""
@@ -209,6 +230,9 @@ class LayerStep:
     def norm_and_queries(self, x, residual, stream=None):
         """residual + x and its normalised rows, and the step's queries from them."""
         st = self.step
+        self._expect(x, (self.T, self.M), "x")
+        if residual is not None:
+            self._expect(residual, (self.T, self.M), "residual")
         if self.fp8:
             mla.mla_add_rmsnorm_fp8(x, residual, self.w["gain"], self.residual, self.hidden, self.codes, self.scales,
                                     self.T, self.M, self.eps, mla.MLA_BF16, stream)

@@ -529,6 +529,25 @@ def test_layer_step_refuses_the_8_bit_cache():
         dec.LayerStep(st, {"gain": torch.ones(64, device=DEV)})
 
 
+def test_layer_step_runs_on_a_stream_other_than_its_constructors():
+    """The 8-bit weights are whole when the constructor returns, though its stream had work queued."""
+    spec, w, st, t, lay = layer_case(64, 1, [70, 5, 129, 1], 1024, "fp8", True)
+    kv0 = st.kv.clone()
+    want = lay.run(t["x"], t["residual"]).clone()
+    st.kv.copy_(kv0)
+    weights = {k: v for k, v in t.items() if k not in ("x", "residual")}
+    busy = bf16(np.ones((8192, 8192)))
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        torch.mm(busy, busy)
+    again = dec.LayerStep(st, weights, projections="fp8")
+    with torch.cuda.stream(other):
+        got = again.run(t["x"], t["residual"], stream=other)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
 # ----------------------------------------------------------------------------- streams
 def test_calls_on_two_streams_at_once():
     """No workspace and no state is shared: calls that overlap on the GPU give what they give alone."""

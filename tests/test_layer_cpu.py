@@ -1,11 +1,14 @@
 """The layer's operators around the attention, on the CPU: pins of their fp64 oracle
 (oracle/layer.py) against library routines and closed forms, and the refusals of the C ABI
 (every call here must fail validation before any launch, or launches nothing)."""
+from types import SimpleNamespace
+
 import numpy as np
 import pytest
 import torch
 
 import mla_latent_kv_46_b200 as mla
+from mla_latent_kv_46_b200.decoder import LayerStep
 from oracle import fp8, layer
 
 INVALID = mla._binding.MLA_ERR_INVALID
@@ -182,3 +185,70 @@ def test_linear_tensor_core_policy_refuses_what_tma_cannot_move(fn, args):
         refused(fn, args, UNSUPPORTED)
     finally:
         mla.mla_set_policy(mla.MLA_POLICY_AUTO)
+
+
+# ----------------------------------------------------------------------------- the layer's step
+class _Step:
+    """What a LayerStep needs of a DecodeStep before it launches anything."""
+
+    def __init__(self, dtype=torch.bfloat16, fp8=False):
+        self.spec = SimpleNamespace(H=64, R=512, Dr=64, Dn=128, Dv=128)
+        self.T, self.fp8, self.device = 3, fp8, torch.device("cpu")
+        self.q_nope = torch.empty(3, 64, 128, dtype=dtype)
+
+
+def _weights(M=96):
+    def empty(*shape):
+        return torch.empty(shape, dtype=torch.bfloat16)
+    return {"gain": empty(M), "W_QN": empty(64 * 128, M), "W_QR": empty(64 * 64, M), "W_DKV": empty(576, M),
+            "kv_gain": empty(512), "W_O": empty(M, 64 * 128), "W_G": empty(64 * 128, M)}
+
+
+def test_layer_step_takes_its_weights():
+    lay = LayerStep(_Step(), _weights())
+    assert lay.gated and lay.M == 96 and lay.y.shape == (3, 96)
+    assert not LayerStep(_Step(), {**_weights(), "W_G": None}).gated
+
+
+@pytest.mark.parametrize("name", sorted(_weights()))
+@pytest.mark.parametrize("change", ["short", "float32", "transposed"])
+def test_layer_step_refuses_a_weight_it_would_misread(name, change):
+    w = _weights()
+    if change == "short":
+        w[name] = w[name][:-1].contiguous()
+    elif change == "float32":
+        w[name] = w[name].float()
+    elif change == "transposed":
+        if w[name].dim() == 1:
+            w[name] = torch.empty(2 * w[name].numel(), dtype=torch.bfloat16)[::2]
+        else:
+            w[name] = torch.empty(*reversed(w[name].shape), dtype=torch.bfloat16).T
+    with pytest.raises(ValueError):
+        LayerStep(_Step(), w)
+
+
+@pytest.mark.parametrize("name", ["W_QN", "W_QR", "W_DKV", "kv_gain", "W_O"])
+def test_layer_step_refuses_a_missing_weight(name):
+    w = _weights()
+    del w[name]
+    with pytest.raises(ValueError):
+        LayerStep(_Step(), w)
+
+
+def test_layer_step_refuses_a_step_in_fp32_or_8_bits():
+    for step in (_Step(dtype=torch.float32), _Step(fp8=True)):
+        with pytest.raises(ValueError):
+            LayerStep(step, _weights())
+    with pytest.raises(ValueError):
+        LayerStep(_Step(), _weights(), projections="fp4")
+
+
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("bad", [torch.empty(2, 96, dtype=torch.bfloat16), torch.empty(3, 96),
+                                 torch.empty(96, 3, dtype=torch.bfloat16).T])
+def test_layer_step_refuses_rows_it_would_misread(which, bad):
+    lay = LayerStep(_Step(), _weights())
+    rows = [torch.empty(3, 96, dtype=torch.bfloat16) for _ in range(2)]
+    rows[which] = bad
+    with pytest.raises(ValueError):
+        lay.run(*rows)
