@@ -98,8 +98,8 @@ template <bool F8>
 __global__ void __launch_bounds__(256) linear_simt_kernel(const void* __restrict__ x, const void* __restrict__ W,
                                                           const Params p) {
   __shared__ float sx[kStep][kTile + 4], sw[kStep][kTile + 4];
-  const int tiles_t = (p.T + kTile - 1) / kTile;
-  const int t0 = (blockIdx.x % tiles_t) * kTile, n0 = (blockIdx.x / tiles_t) * kTile;
+  const unsigned tiles_t = ((unsigned)p.T + kTile - 1) / kTile;      // T may be all of 31 bits
+  const int t0 = (int)(blockIdx.x % tiles_t) * kTile, n0 = (int)(blockIdx.x / tiles_t) * kTile;
   const int tid = threadIdx.x;
   const int ty = tid / 16, tx = tid % 16;     // tokens 4 ty .., features tx, tx + 16, ..
   auto fetch = [&](const void* base, int64_t row, int64_t rows, int k) -> float {
