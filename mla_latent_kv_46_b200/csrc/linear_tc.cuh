@@ -156,6 +156,10 @@ __device__ __forceinline__ void prefetch_rows(const Params& p, int64_t t0, int c
   }
 }
 
+__device__ __forceinline__ float half_of(uint32_t two, int which) {
+  return __uint_as_float(which ? two & 0xFFFF0000u : two << 16);
+}
+
 // ------------------------------------------------------------------ shared by both kernels
 constexpr int kMaxStages = 12;
 // How long a kernel that gave up waits for its own copies and MMAs in flight, which land
@@ -463,10 +467,13 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
 // TMA, was no faster: 4096 x 7168 x 512 with a residual and a sigmoid 67 against 58 us.)
 constexpr int kEpiWarps = 8, kEpiSets = kEpiWarps / 4;
 constexpr int kPairThreads = 32 * (4 + kEpiWarps);
-// behind the ring: per epilogue warp, its tile's token scales (8-bit operands)
+// behind the ring: per epilogue warp, its tile's token scales (8-bit operands), and, in the WIDE
+// kernel, kRing stages of an 8 token x 32 feature tile of mul and of residual
 constexpr int kScaleBytes = kEpiWarps * 256 * 4;
-__host__ __device__ constexpr int pair_smem(int nt, int stages) {
-  return stages * stage_bytes_of(nt) + kScaleBytes + kSmemSlack;
+constexpr int kOctTokens = 8, kOctBytes = kOctTokens * 32 * 2, kRing = 3;
+__host__ __device__ constexpr int wide_bytes(bool wide) { return wide ? kEpiWarps * kRing * 2 * kOctBytes : 0; }
+__host__ __device__ constexpr int pair_smem(int nt, int stages, bool wide) {
+  return stages * stage_bytes_of(nt) + kScaleBytes + wide_bytes(wide) + kSmemSlack;
 }
 static_assert(8 * (2 * kMaxStages + 5) + 16 <= kBarBytes, "barriers");
 
@@ -486,7 +493,7 @@ __device__ __forceinline__ TileAt tile_of(uint32_t i, uint32_t tiles_n, uint32_t
   return TileAt{(int)(rem / width), (int)(first + rem % width)};
 }
 
-template <bool F8>
+template <bool F8, bool WIDE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Params p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -496,7 +503,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
   // CTA), accumulator free (even CTA: both CTAs' epilogue warps)
   const int nt = p.nt, stages = p.stages;
   const uint32_t stage_bytes = (uint32_t)stage_bytes_of(nt);
-  const int off_scale = stages * (int)stage_bytes, off_bar = off_scale + kScaleBytes;
+  const int off_scale = stages * (int)stage_bytes, off_ring = off_scale + kScaleBytes;
+  const int off_bar = off_ring + wide_bytes(WIDE);
   auto bar = [&](int i) { return sbase + off_bar + 8u * i; };
   const int kFull = 0, kEmpty = stages, kAccFull = 2 * stages, kAccFree = 2 * stages + 2;
   const int kDrain = 2 * stages + 4, kOffMisc = off_bar + 8 * (kDrain + 1);
@@ -640,6 +648,12 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
       if (p.mul || p.res) prefetch_rows(p, t.t0, t.tokens, t.nw, 32, set, kEpiSets, lane);
     };
     float* scale = reinterpret_cast<float*>(smem + off_scale) + (warp - 4) * 256;
+    // WIDE: a chunk lies [token][feature] in a stage's place, 64 bytes a token, whose 16-byte pieces are
+    // turned by the token so that neither access has a bank conflict: lane / 4 is the token and lane %
+    // 4 the piece of the 16-byte accesses, lane % 8 and lane / 8 those of the matrix ones.
+    const uint32_t ring = sbase + off_ring + (warp - 4) * (kRing * 2 * kOctBytes);
+    auto place = [](int token, int piece) { return (uint32_t)(64 * token + 16 * (piece ^ (token / 2 % 4))); };
+    const uint32_t vec_off = place(lane / 4, lane % 4), mat_off = place(lane % 8, lane / 8);
     int u = 0;
     Tile t = tile_at(min(pair, tiles - 1)), after = t;
     prefetch(t);
@@ -647,9 +661,6 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
       const int b = u & 1;
       t = after;
       if (i + pairs < tiles) after = tile_at(i + pairs);
-      const int32_t n = t.nw + lane;
-      const float bias = p.bias && n < p.N ? __bfloat162float(p.bias[n]) : 0.f;
-      const float ws = F8 && n < p.N ? scale_of(p.ws[n]) : 1.f;
       if (F8) {
         __syncwarp();      // the tile before is read
 #pragma unroll
@@ -659,35 +670,120 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         }
         __syncwarp();
       }
-      const uint32_t trow = tbase + ((32u * q) << 16) + b * nt;
-      const int64_t step = (int64_t)kEpiSets * kChunk * p.N;
-      int c = kChunk * set;
-      int64_t at = (t.t0 + c) * p.N + n;
-      // a chunk's operands are loaded before the chunk before it is finished
-      Operands<kChunk> ops, next;
-      if (c < t.tokens && n < p.N) ops.load(p, at, t.tokens - c);
-      if (!wait_all(bar(kAccFull + b), (uint32_t)((u >> 1) & 1))) { give_up(); break; }
-      ptx::tc_fence_after();
-      if (i + pairs < tiles) prefetch(after);      // its main loop is beginning
-#pragma unroll 2
-      for (; c < t.tokens; c += kEpiSets * kChunk, at += step) {
-        float v[kChunk];
-        ptx::tmem_ld_32x32b_x16(trow + c, v);
-        const int left = t.tokens - c, then = left - kEpiSets * kChunk;
-        if (then > 0 && n < p.N) next.load(p, at + step, then);
-        float sx[kChunk];
-        if (F8) {
+      if constexpr (WIDE) {
+        const int tok = lane / 4;
+        const int32_t n = t.nw + 8 * (lane % 4);
+        float bias[4], ws[4];      // of features nw + lane / 4 + 8 m
 #pragma unroll
-          for (int j = 0; j < kChunk; j += 4)
-            *reinterpret_cast<float4*>(sx + j) = *reinterpret_cast<const float4*>(scale + c + j);
+        for (int m = 0; m < 4; ++m) {
+          const int32_t f = t.nw + lane / 4 + 8 * m;
+          bias[m] = p.bias && f < p.N ? __bfloat162float(p.bias[f]) : 0.f;
+          ws[m] = F8 && f < p.N ? scale_of(p.ws[f]) : 1.f;
         }
-        ptx::tmem_wait_ld();
-        if (n < p.N) finish_tokens<F8, kChunk>(p, v, ops, at, left, bias, ws, sx);
-        ops = next;
-        __syncwarp();
+        const uint32_t trow = tbase + ((32u * q) << 16) + b * nt;
+        const bool operands = p.mul || p.res;
+        constexpr int kSweep = kEpiSets * kOctTokens;
+        int c = kOctTokens * set, slot = 0;
+        const int64_t step = (int64_t)kSweep * p.N;
+        int64_t at = (t.t0 + c + tok) * p.N + n;
+        // the operands of the chunk from token c on into stage `into`, one group of copies (empty
+        // past the tile's tokens)
+        auto fetch = [&](int c, int64_t at, int into) {
+          const uint32_t dst = ring + into * (2 * kOctBytes) + vec_off;
+          if (n < p.N && c + tok < t.tokens) {
+            if (p.mul) ptx::copy16_async(dst, p.mul + at);
+            if (p.res) ptx::copy16_async(dst + kOctBytes, p.res + at);
+          }
+          ptx::copy_commit();
+        };
+        if (operands) {
+          fetch(c, at, 0);
+          fetch(c + kSweep, at + step, 1);
+        }
+        if (!wait_all(bar(kAccFull + b), (uint32_t)((u >> 1) & 1))) { give_up(); break; }
+        ptx::tc_fence_after();
+        if (i + pairs < tiles) prefetch(after);      // its main loop is beginning
+#pragma unroll 1
+        for (; c < t.tokens; c += kSweep, at += step) {
+          float v[8];      // feature lane / 4 + 8 m, tokens c + 2 (lane % 4) + {0, 1}: v[2 m ..]
+          ptx::tmem_ld_16x256b_x1(trow + c, v);
+          ptx::tmem_ld_16x256b_x1(trow + (16u << 16) + c, v + 4);
+          const uint32_t tile = ring + slot * (2 * kOctBytes);
+          if (operands) {
+            fetch(c + 2 * kSweep, at + 2 * step, slot == 0 ? 2 : slot - 1);
+            ptx::copy_wait<2>();
+            __syncwarp();
+          }
+          ptx::tmem_wait_ld();
+          if (F8) {
+            const float2 sx = *reinterpret_cast<const float2*>(scale + c + 2 * (lane % 4));
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+              v[2 * m] = v[2 * m] * ws[m] * sx.x;
+              v[2 * m + 1] = v[2 * m + 1] * ws[m] * sx.y;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] += bias[e / 2];
+          activate(v, p.act);
+          uint32_t w[4];
+          if (p.mul) {
+            ptx::ldmatrix_x4_trans(tile + mat_off, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= half_of(w[e / 2], e % 2);
+          }
+          if (p.res) {
+            ptx::ldmatrix_x4_trans(tile + kOctBytes + mat_off, w);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] += half_of(w[e / 2], e % 2);
+          }
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * m], v[2 * m + 1]);
+            w[m] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+          __syncwarp();      // mul is read: its place takes the results
+          ptx::stmatrix_x4_trans(tile + mat_off, w);
+          __syncwarp();
+          if (n < p.N && c + tok < t.tokens) *reinterpret_cast<uint4*>(p.out + at) = ptx::ld_shared_v4(tile + vec_off);
+          __syncwarp();
+          slot = slot == kRing - 1 ? 0 : slot + 1;
+        }
+      } else {
+        const int32_t n = t.nw + lane;
+        const float bias = p.bias && n < p.N ? __bfloat162float(p.bias[n]) : 0.f;
+        const float ws = F8 && n < p.N ? scale_of(p.ws[n]) : 1.f;
+        const uint32_t trow = tbase + ((32u * q) << 16) + b * nt;
+        const int64_t step = (int64_t)kEpiSets * kChunk * p.N;
+        int c = kChunk * set;
+        int64_t at = (t.t0 + c) * p.N + n;
+        // a chunk's operands are loaded before the chunk before it is finished
+        Operands<kChunk> ops, next;
+        if (c < t.tokens && n < p.N) ops.load(p, at, t.tokens - c);
+        if (!wait_all(bar(kAccFull + b), (uint32_t)((u >> 1) & 1))) { give_up(); break; }
+        ptx::tc_fence_after();
+        if (i + pairs < tiles) prefetch(after);      // its main loop is beginning
+#pragma unroll 2
+        for (; c < t.tokens; c += kEpiSets * kChunk, at += step) {
+          float v[kChunk];
+          ptx::tmem_ld_32x32b_x16(trow + c, v);
+          const int left = t.tokens - c, then = left - kEpiSets * kChunk;
+          if (then > 0 && n < p.N) next.load(p, at + step, then);
+          float sx[kChunk];
+          if (F8) {
+#pragma unroll
+            for (int j = 0; j < kChunk; j += 4)
+              *reinterpret_cast<float4*>(sx + j) = *reinterpret_cast<const float4*>(scale + c + j);
+          }
+          ptx::tmem_wait_ld();
+          if (n < p.N) finish_tokens<F8, kChunk>(p, v, ops, at, left, bias, ws, sx);
+          ops = next;
+          __syncwarp();
+        }
       }
       release(b);
     }
+    if (WIDE) ptx::copy_wait<0>();      // (after a wait that ran out)
   }
   __syncthreads();
   ptx::cluster_sync();   // the even CTA's MMAs, commits and loads for both CTAs are done

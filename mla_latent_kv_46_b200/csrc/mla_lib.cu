@@ -1457,20 +1457,20 @@ mla_status launch_linear_split(const void* x, const void* W, mla::lin::Params p,
                            split_smem(nt, p.stages, slices), 2 * slices, st, tw, tx, p);
 }
 
-template <bool F8>
+template <bool F8, bool WIDE>
 mla_status launch_linear_pair(const void* x, const void* W, mla::lin::Params p, int nt, int32_t sms, cudaStream_t st,
                               const char* what) {
   using namespace mla::lin;
-  auto kern = linear_pair_kernel<F8>;
+  auto kern = linear_pair_kernel<F8, WIDE>;
   CUtensorMap tw, tx;
   if (mla_status s = linear_maps<F8>(&tw, &tx, W, x, p, kM, (uint32_t)nt / 2)) return s;
   if (mla_status s = ensure_smem_attr((const void*)kern, kSmemOfOne)) return s;
   p.nt = nt;
-  p.stages = std::min(kMaxStages, (kSmemOfOne - pair_smem(nt, 0)) / stage_bytes_of(nt));
+  p.stages = std::min(kMaxStages, (kSmemOfOne - pair_smem(nt, 0, WIDE)) / stage_bytes_of(nt));
   const int64_t tiles = (((int64_t)p.N + 2 * kM - 1) / (2 * kM)) * (((int64_t)p.T + nt - 1) / nt);
   if (tiles > 0x7FFF0000) return fail(MLA_ERR_UNSUPPORTED, "%s: T=%d N=%d is too large", what, p.T, p.N);
   const unsigned pairs = (unsigned)std::min<int64_t>(tiles, std::max(1, sms / 2));
-  return launch_overlapped(what, kern, dim3(2 * pairs), kPairThreads, pair_smem(nt, p.stages), 0, st, tw, tx, p);
+  return launch_overlapped(what, kern, dim3(2 * pairs), kPairThreads, pair_smem(nt, p.stages, WIDE), 0, st, tw, tx, p);
 }
 
 // Which kernel, tokens per tile and K slices. Both kernels' times are estimated from the sizes
@@ -1536,8 +1536,10 @@ template <bool F8>
 mla_status linear_tc(const void* x, const void* W, const mla::lin::Params& p, cudaStream_t st, const char* what) {
   const int32_t sms = device_sms();
   const LinearChoice c = choose_linear(p, F8, sms);
-  return c.pair ? launch_linear_pair<F8>(x, W, p, c.nt, sms, st, what)
-                : launch_linear_split<F8>(x, W, p, c.nt, c.slices, sms, st, what);
+  if (c.pair)
+    return p.octs ? launch_linear_pair<F8, true>(x, W, p, c.nt, sms, st, what)
+                  : launch_linear_pair<F8, false>(x, W, p, c.nt, sms, st, what);
+  return launch_linear_split<F8>(x, W, p, c.nt, c.slices, sms, st, what);
 }
 
 mla_status linear(const char* what, bool f8, const void* x, const void* xs, const void* W, const void* ws,
