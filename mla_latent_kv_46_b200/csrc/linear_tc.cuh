@@ -465,15 +465,14 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
 // alignment). Where K is short the epilogue is what a tile takes: its instructions count.
 // (Turning the sums through shared memory into 16-byte accesses, with the operands brought by
 // TMA, was no faster: 4096 x 7168 x 512 with a residual and a sigmoid 67 against 58 us.)
-constexpr int kEpiWarps = 8, kEpiSets = kEpiWarps / 4;
-constexpr int kPairThreads = 32 * (4 + kEpiWarps);
-// behind the ring: per epilogue warp, its tile's token scales (8-bit operands), and, in the WIDE
-// kernel, kRing stages of an 8 token x 32 feature tile of mul and of residual
-constexpr int kScaleBytes = kEpiWarps * 256 * 4;
-constexpr int kOctTokens = 8, kOctBytes = kOctTokens * 32 * 2, kRing = 3;
-__host__ __device__ constexpr int wide_bytes(bool wide) { return wide ? kEpiWarps * kRing * 2 * kOctBytes : 0; }
+__host__ __device__ constexpr int epi_warps(bool wide) { return wide ? 16 : 8; }
+__host__ __device__ constexpr int pair_threads(bool wide) { return 32 * (4 + epi_warps(wide)); }
+// Behind the ring, per epilogue warp: its tile's token scales (8-bit operands); in the WIDE kernel
+// kSlots places for an 8 token x 32 feature piece of mul, residual or the results.
+constexpr int kOctTokens = 8, kSlotBytes = kOctTokens * 32 * 2, kSlots = 4;
+__host__ __device__ constexpr int epi_bytes(bool wide) { return epi_warps(wide) * (wide ? kSlots * kSlotBytes : 256 * 4); }
 __host__ __device__ constexpr int pair_smem(int nt, int stages, bool wide) {
-  return stages * stage_bytes_of(nt) + kScaleBytes + wide_bytes(wide) + kSmemSlack;
+  return stages * stage_bytes_of(nt) + epi_bytes(wide) + kSmemSlack;
 }
 static_assert(8 * (2 * kMaxStages + 5) + 16 <= kBarBytes, "barriers");
 
@@ -494,7 +493,7 @@ __device__ __forceinline__ TileAt tile_of(uint32_t i, uint32_t tiles_n, uint32_t
 }
 
 template <bool F8, bool WIDE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(pair_threads(WIDE), 1)
 linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const Params p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -503,8 +502,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
   // CTA), accumulator free (even CTA: both CTAs' epilogue warps)
   const int nt = p.nt, stages = p.stages;
   const uint32_t stage_bytes = (uint32_t)stage_bytes_of(nt);
-  const int off_scale = stages * (int)stage_bytes, off_ring = off_scale + kScaleBytes;
-  const int off_bar = off_ring + wide_bytes(WIDE);
+  const int off_epi = stages * (int)stage_bytes, off_bar = off_epi + epi_bytes(WIDE);
+  constexpr int kEpiWarps = epi_warps(WIDE), kEpiSets = kEpiWarps / 4;
   auto bar = [&](int i) { return sbase + off_bar + 8u * i; };
   const int kFull = 0, kEmpty = stages, kAccFull = 2 * stages, kAccFree = 2 * stages + 2;
   const int kDrain = 2 * stages + 4, kOffMisc = off_bar + 8 * (kDrain + 1);
@@ -645,13 +644,28 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     };
     // this warp's share of a tile's operands into L2, a tile ahead
     auto prefetch = [&](const Tile& t) {
-      if (p.mul || p.res) prefetch_rows(p, t.t0, t.tokens, t.nw, 32, set, kEpiSets, lane);
+      if constexpr (WIDE) {      // a CTA's 128 features of a token at a time
+        const int32_t n0 = t.nw - 32 * q;
+        const uint32_t bytes = 2u * (uint32_t)min(kM, p.N - n0);
+        if (n0 < p.N)
+          for (int j = (warp - 4) * 32 + lane; j < t.tokens; j += 32 * kEpiWarps) {
+            const int64_t at = (t.t0 + j) * p.N + n0;
+            if (p.mul) ptx::prefetch_l2_bulk(p.mul + at, bytes);
+            if (p.res) ptx::prefetch_l2_bulk(p.res + at, bytes);
+          }
+      } else if (p.mul || p.res) {
+        prefetch_rows(p, t.t0, t.tokens, t.nw, 32, set, kEpiSets, lane);
+      }
     };
-    float* scale = reinterpret_cast<float*>(smem + off_scale) + (warp - 4) * 256;
-    // WIDE: a chunk lies [token][feature] in a stage's place, 64 bytes a token, whose 16-byte pieces are
+    float* scale = reinterpret_cast<float*>(smem + off_epi) + (warp - 4) * 256;      // not WIDE
+    // WIDE: a piece lies [token][feature] in its place, 64 bytes a token, whose 16-byte parts are
     // turned by the token so that neither access has a bank conflict: lane / 4 is the token and lane %
-    // 4 the piece of the 16-byte accesses, lane % 8 and lane / 8 those of the matrix ones.
-    const uint32_t ring = sbase + off_ring + (warp - 4) * (kRing * 2 * kOctBytes);
+    // 4 the part of the 16-byte accesses, lane % 8 and lane / 8 those of the matrix ones. With one
+    // operand three pieces are on their way behind the one at work, with two one.
+    const uint32_t slots = sbase + off_epi + (warp - 4) * (kSlots * kSlotBytes);
+    const bool operands = p.mul || p.res, both = p.mul && p.res;
+    const int ahead = both ? kSlots / 2 - 1 : kSlots - 1;
+    const uint32_t piece_bytes = both ? 2 * kSlotBytes : kSlotBytes, res_off = both ? kSlotBytes : 0;
     auto place = [](int token, int piece) { return (uint32_t)(64 * token + 16 * (piece ^ (token / 2 % 4))); };
     const uint32_t vec_off = place(lane / 4, lane % 4), mat_off = place(lane % 8, lane / 8);
     int u = 0;
@@ -661,15 +675,6 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
       const int b = u & 1;
       t = after;
       if (i + pairs < tiles) after = tile_at(i + pairs);
-      if (F8) {
-        __syncwarp();      // the tile before is read
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int j = 32 * k + lane;
-          scale[j] = j < t.tokens ? scale_of(p.xs[t.t0 + j]) : 0.f;
-        }
-        __syncwarp();
-      }
       if constexpr (WIDE) {
         const int tok = lane / 4;
         const int32_t n = t.nw + 8 * (lane % 4);
@@ -681,59 +686,67 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
           ws[m] = F8 && f < p.N ? scale_of(p.ws[f]) : 1.f;
         }
         const uint32_t trow = tbase + ((32u * q) << 16) + b * nt;
-        const bool operands = p.mul || p.res;
         constexpr int kSweep = kEpiSets * kOctTokens;
-        int c = kOctTokens * set, slot = 0;
+        int c = kOctTokens * set, k = 0;
         const int64_t step = (int64_t)kSweep * p.N;
         int64_t at = (t.t0 + c + tok) * p.N + n;
-        // the operands of the chunk from token c on into stage `into`, one group of copies (empty
-        // past the tile's tokens)
-        auto fetch = [&](int c, int64_t at, int into) {
-          const uint32_t dst = ring + into * (2 * kOctBytes) + vec_off;
-          if (n < p.N && c + tok < t.tokens) {
-            if (p.mul) ptx::copy16_async(dst, p.mul + at);
-            if (p.res) ptx::copy16_async(dst + kOctBytes, p.res + at);
+        // operands of the piece `far` sweeps from here, one group of copies (empty past the tile's tokens)
+        auto fetch = [&](int far, int into) {
+          const uint32_t dst = slots + (into & ahead) * piece_bytes + vec_off;
+          if (n < p.N && c + far * kSweep + tok < t.tokens) {
+            if (p.mul) ptx::copy16_async(dst, p.mul + at + far * step);
+            if (p.res) ptx::copy16_async(dst + res_off, p.res + at + far * step);
           }
           ptx::copy_commit();
         };
-        if (operands) {
-          fetch(c, at, 0);
-          fetch(c + kSweep, at + step, 1);
-        }
+        // scale bytes of the two tokens of a piece whose values this thread has
+        auto scales_of = [&](int c) {
+          const int j = c + 2 * (lane % 4);
+          uchar2 two = make_uchar2(0, 0);
+          if (F8 && j < t.tokens) two.x = p.xs[t.t0 + j];
+          if (F8 && j + 1 < t.tokens) two.y = p.xs[t.t0 + j + 1];
+          return two;
+        };
+        uchar2 sx = scales_of(c);
+        if (operands)
+          for (int far = 0; far < ahead; ++far) fetch(far, far);
         if (!wait_all(bar(kAccFull + b), (uint32_t)((u >> 1) & 1))) { give_up(); break; }
         ptx::tc_fence_after();
         if (i + pairs < tiles) prefetch(after);      // its main loop is beginning
 #pragma unroll 1
-        for (; c < t.tokens; c += kSweep, at += step) {
+        for (; c < t.tokens; c += kSweep, at += step, ++k) {
           float v[8];      // feature lane / 4 + 8 m, tokens c + 2 (lane % 4) + {0, 1}: v[2 m ..]
           ptx::tmem_ld_16x256b_x1(trow + c, v);
           ptx::tmem_ld_16x256b_x1(trow + (16u << 16) + c, v + 4);
-          const uint32_t tile = ring + slot * (2 * kOctBytes);
+          const uint32_t piece = slots + (k & ahead) * piece_bytes;
           if (operands) {
-            fetch(c + 2 * kSweep, at + 2 * step, slot == 0 ? 2 : slot - 1);
-            ptx::copy_wait<2>();
+            fetch(ahead, k + ahead);
+            if (both) ptx::copy_wait<kSlots / 2 - 1>();
+            else ptx::copy_wait<kSlots - 1>();
             __syncwarp();
           }
+          const uchar2 next = scales_of(c + kSweep);
           ptx::tmem_wait_ld();
           if (F8) {
-            const float2 sx = *reinterpret_cast<const float2*>(scale + c + 2 * (lane % 4));
+            const float x0 = scale_of(sx.x), x1 = scale_of(sx.y);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
-              v[2 * m] = v[2 * m] * ws[m] * sx.x;
-              v[2 * m + 1] = v[2 * m + 1] * ws[m] * sx.y;
+              v[2 * m] = v[2 * m] * ws[m] * x0;
+              v[2 * m + 1] = v[2 * m + 1] * ws[m] * x1;
             }
+            sx = next;
           }
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] += bias[e / 2];
           activate(v, p.act);
           uint32_t w[4];
           if (p.mul) {
-            ptx::ldmatrix_x4_trans(tile + mat_off, w);
+            ptx::ldmatrix_x4_trans(piece + mat_off, w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] *= half_of(w[e / 2], e % 2);
           }
           if (p.res) {
-            ptx::ldmatrix_x4_trans(tile + kOctBytes + mat_off, w);
+            ptx::ldmatrix_x4_trans(piece + res_off + mat_off, w);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] += half_of(w[e / 2], e % 2);
           }
@@ -742,14 +755,22 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
             const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * m], v[2 * m + 1]);
             w[m] = *reinterpret_cast<const uint32_t*>(&h);
           }
-          __syncwarp();      // mul is read: its place takes the results
-          ptx::stmatrix_x4_trans(tile + mat_off, w);
+          __syncwarp();      // the operand is read: its place takes the results
+          ptx::stmatrix_x4_trans(piece + mat_off, w);
           __syncwarp();
-          if (n < p.N && c + tok < t.tokens) *reinterpret_cast<uint4*>(p.out + at) = ptx::ld_shared_v4(tile + vec_off);
+          if (n < p.N && c + tok < t.tokens) *reinterpret_cast<uint4*>(p.out + at) = ptx::ld_shared_v4(piece + vec_off);
           __syncwarp();
-          slot = slot == kRing - 1 ? 0 : slot + 1;
         }
       } else {
+        if (F8) {
+          __syncwarp();      // the tile before is read
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int j = 32 * k + lane;
+            scale[j] = j < t.tokens ? scale_of(p.xs[t.t0 + j]) : 0.f;
+          }
+          __syncwarp();
+        }
         const int32_t n = t.nw + lane;
         const float bias = p.bias && n < p.N ? __bfloat162float(p.bias[n]) : 0.f;
         const float ws = F8 && n < p.N ? scale_of(p.ws[n]) : 1.f;

@@ -1470,7 +1470,7 @@ mla_status launch_linear_pair(const void* x, const void* W, mla::lin::Params p, 
   const int64_t tiles = (((int64_t)p.N + 2 * kM - 1) / (2 * kM)) * (((int64_t)p.T + nt - 1) / nt);
   if (tiles > 0x7FFF0000) return fail(MLA_ERR_UNSUPPORTED, "%s: T=%d N=%d is too large", what, p.T, p.N);
   const unsigned pairs = (unsigned)std::min<int64_t>(tiles, std::max(1, sms / 2));
-  return launch_overlapped(what, kern, dim3(2 * pairs), kPairThreads, pair_smem(nt, p.stages, WIDE), 0, st, tw, tx, p);
+  return launch_overlapped(what, kern, dim3(2 * pairs), pair_threads(WIDE), pair_smem(nt, p.stages, WIDE), 0, st, tw, tx, p);
 }
 
 // Which kernel, tokens per tile and K slices. Both kernels' times are estimated from the sizes
