@@ -44,23 +44,38 @@ __device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + __ex
 // exponential is 0 in fp32). The exponent's roundings (x^2, and its product with log2(e) / 2)
 // are carried to first order, or they would be 1e-5 of the tail. All in all 1e-6 of the result;
 // erfcf took twice the time of a 4685 x 2802 output's whole epilogue.
-__device__ __forceinline__ float gelu(float v) {
-  const float x = fminf(fabsf(v), 20.f);      // above, Q is 0 as well; keeps x^2 finite
-  const float t = __fdividef(1.f, fmaf(0.35f, x, 1.f));
-  float r = -0.029146350920200348f;
-  r = fmaf(r, t, 0.143973708152771f);
-  r = fmaf(r, t, -0.25571832060813904f);
-  r = fmaf(r, t, 0.1591787040233612f);
-  r = fmaf(r, t, -0.02311287634074688f);
-  r = fmaf(r, t, 0.10550924390554428f);
-  r = fmaf(r, t, 0.11983256787061691f);
-  r = fmaf(r, t, 0.13986191153526306f);
-  r = fmaf(r, t, 0.13962140679359436f);
-  const float c = 0.72134752f, c_lo = 9.629815167500055e-09f;
-  const float s = x * x, s_lo = fmaf(x, x, -s);
-  const float y = s * c, y_lo = fmaf(s, c_lo, fmaf(s, c, -y));
-  const float q = ptx::ex2(-y) * (r * t) * fmaf(-0.5f, s_lo, fmaf(-0.69314718f, y_lo, 1.f));
-  return v * (v > 0.f ? 1.f - q : q);
+// Two elements at a time: all but the exponential, the quotient and the choice of the side
+// are paired instructions.
+__device__ __forceinline__ void gelu(float& v0, float& v1) {
+  using ptx::F2;
+  auto both = [](float c) { return ptx::f2(c, c); };
+  const float x0 = fminf(fabsf(v0), 20.f), x1 = fminf(fabsf(v1), 20.f);      // above, Q is 0 as well; keeps x^2 finite
+  const F2 x = ptx::f2(x0, x1), minus = both(-1.f);
+  float d0, d1;
+  ptx::split(ptx::fma2(both(0.35f), x, both(1.f)), d0, d1);
+  const F2 t = ptx::f2(__fdividef(1.f, d0), __fdividef(1.f, d1));
+  F2 r = both(-0.029146350920200348f);
+  r = ptx::fma2(r, t, both(0.143973708152771f));
+  r = ptx::fma2(r, t, both(-0.25571832060813904f));
+  r = ptx::fma2(r, t, both(0.1591787040233612f));
+  r = ptx::fma2(r, t, both(-0.02311287634074688f));
+  r = ptx::fma2(r, t, both(0.10550924390554428f));
+  r = ptx::fma2(r, t, both(0.11983256787061691f));
+  r = ptx::fma2(r, t, both(0.13986191153526306f));
+  r = ptx::fma2(r, t, both(0.13962140679359436f));
+  // s = -x^2 and y = s log2(e) / 2, each with what its rounding left
+  const F2 c = both(0.72134752f), c_lo = both(9.629815167500055e-09f);
+  const F2 s = ptx::mul2(x, ptx::mul2(x, minus)), s_lo = ptx::fma2(x, x, s);
+  const F2 y = ptx::mul2(s, c), y_lo = ptx::fma2(s, c_lo, ptx::fma2(s, c, ptx::mul2(y, minus)));
+  float y0, y1, q0, q1, u0, u1;
+  ptx::split(y, y0, y1);
+  const F2 e = ptx::f2(ptx::ex2(y0), ptx::ex2(y1));
+  const F2 q = ptx::mul2(ptx::mul2(e, ptx::mul2(r, t)),
+                         ptx::fma2(both(-0.5f), s_lo, ptx::fma2(both(0.69314718f), y_lo, both(1.f))));
+  ptx::split(q, q0, q1);
+  ptx::split(ptx::fma2(q, minus, both(1.f)), u0, u1);
+  v0 *= v0 > 0.f ? u0 : q0;
+  v1 *= v1 > 0.f ? u1 : q1;
 }
 // All of a thread's elements: one branch, straight code behind it (a branch per element of an
 // unrolled epilogue ran out of the instruction cache).
@@ -74,7 +89,11 @@ __device__ __forceinline__ void activate(float (&v)[CNT], int act) {
     for (int j = 0; j < CNT; ++j) v[j] = silu(v[j]);
   } else if (act == kActGelu) {
 #pragma unroll
-    for (int j = 0; j < CNT; ++j) v[j] = gelu(v[j]);
+    for (int j = 0; j + 1 < CNT; j += 2) gelu(v[j], v[j + 1]);
+    if (CNT % 2) {
+      float other = 0.f;
+      gelu(v[CNT - 1], other);
+    }
   }
 }
 

@@ -156,8 +156,9 @@ __device__ __forceinline__ void prefetch_rows(const Params& p, int64_t t0, int c
   }
 }
 
-__device__ __forceinline__ float half_of(uint32_t two, int which) {
-  return __uint_as_float(which ? two & 0xFFFF0000u : two << 16);
+// Two bf16 values.
+__device__ __forceinline__ ptx::F2 halves(uint32_t two) {
+  return ptx::f2(__uint_as_float(two << 16), __uint_as_float(two & 0xFFFF0000u));
 }
 
 // ------------------------------------------------------------------ shared by both kernels
@@ -708,6 +709,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
           return two;
         };
         uchar2 sx = scales_of(c);
+        __syncwarp();      // the tile before is read
         if (operands)
           for (int far = 0; far < ahead; ++far) fetch(far, far);
         if (!wait_all(bar(kAccFull + b), (uint32_t)((u >> 1) & 1))) { give_up(); break; }
@@ -720,46 +722,44 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
           ptx::tmem_ld_16x256b_x1(trow + (16u << 16) + c, v + 4);
           const uint32_t piece = slots + (k & ahead) * piece_bytes;
           if (operands) {
+            if (both) ptx::copy_wait<kSlots / 2 - 2>();
+            else ptx::copy_wait<kSlots - 2>();
+            __syncwarp();      // and every lane has read the results from the place that is filled next
             fetch(ahead, k + ahead);
-            if (both) ptx::copy_wait<kSlots / 2 - 1>();
-            else ptx::copy_wait<kSlots - 1>();
-            __syncwarp();
           }
           const uchar2 next = scales_of(c + kSweep);
           ptx::tmem_wait_ld();
-          if (F8) {
-            const float x0 = scale_of(sx.x), x1 = scale_of(sx.y);
+          const ptx::F2 x = ptx::f2(scale_of(sx.x), scale_of(sx.y));
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-              v[2 * m] = v[2 * m] * ws[m] * x0;
-              v[2 * m + 1] = v[2 * m + 1] * ws[m] * x1;
-            }
-            sx = next;
+          for (int m = 0; m < 4; ++m) {
+            ptx::F2 two = ptx::f2(v[2 * m], v[2 * m + 1]);
+            if (F8) two = ptx::mul2(ptx::mul2(two, ptx::f2(ws[m], ws[m])), x);
+            ptx::split(ptx::add2(two, ptx::f2(bias[m], bias[m])), v[2 * m], v[2 * m + 1]);
           }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] += bias[e / 2];
+          sx = next;
           activate(v, p.act);
           uint32_t w[4];
           if (p.mul) {
             ptx::ldmatrix_x4_trans(piece + mat_off, w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] *= half_of(w[e / 2], e % 2);
+            for (int m = 0; m < 4; ++m)
+              ptx::split(ptx::mul2(ptx::f2(v[2 * m], v[2 * m + 1]), halves(w[m])), v[2 * m], v[2 * m + 1]);
           }
           if (p.res) {
             ptx::ldmatrix_x4_trans(piece + res_off + mat_off, w);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v[e] += half_of(w[e / 2], e % 2);
+            for (int m = 0; m < 4; ++m)
+              ptx::split(ptx::add2(ptx::f2(v[2 * m], v[2 * m + 1]), halves(w[m])), v[2 * m], v[2 * m + 1]);
           }
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * m], v[2 * m + 1]);
             w[m] = *reinterpret_cast<const uint32_t*>(&h);
           }
-          __syncwarp();      // the operand is read: its place takes the results
+          if (operands) __syncwarp();      // the operand is read: its place takes the results
           ptx::stmatrix_x4_trans(piece + mat_off, w);
           __syncwarp();
           if (n < p.N && c + tok < t.tokens) *reinterpret_cast<uint4*>(p.out + at) = ptx::ld_shared_v4(piece + vec_off);
-          __syncwarp();
         }
       } else {
         if (F8) {
