@@ -645,18 +645,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     };
     // this warp's share of a tile's operands into L2, a tile ahead
     auto prefetch = [&](const Tile& t) {
-      if constexpr (WIDE) {      // a CTA's 128 features of a token at a time
-        const int32_t n0 = t.nw - 32 * q;
-        const uint32_t bytes = 2u * (uint32_t)min(kM, p.N - n0);
-        if (n0 < p.N)
-          for (int j = (warp - 4) * 32 + lane; j < t.tokens; j += 32 * kEpiWarps) {
-            const int64_t at = (t.t0 + j) * p.N + n0;
-            if (p.mul) ptx::prefetch_l2_bulk(p.mul + at, bytes);
-            if (p.res) ptx::prefetch_l2_bulk(p.res + at, bytes);
-          }
-      } else if (p.mul || p.res) {
-        prefetch_rows(p, t.t0, t.tokens, t.nw, 32, set, kEpiSets, lane);
-      }
+      if (!WIDE && (p.mul || p.res)) prefetch_rows(p, t.t0, t.tokens, t.nw, 32, set, kEpiSets, lane);
     };
     float* scale = reinterpret_cast<float*>(smem + off_epi) + (warp - 4) * 256;      // not WIDE
     // WIDE: a piece lies [token][feature] in its place, 64 bytes a token, whose 16-byte parts are
@@ -691,12 +680,13 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         int c = kOctTokens * set, k = 0;
         const int64_t step = (int64_t)kSweep * p.N;
         int64_t at = (t.t0 + c + tok) * p.N + n;
-        // operands of the piece `far` sweeps from here, one group of copies (empty past the tile's tokens)
-        auto fetch = [&](int far, int into) {
+        // operands of the piece from token c on, one group of copies (empty past the tile's tokens)
+        const int own = n < p.N ? t.tokens - tok : 0;      // pieces before it have this thread's token
+        auto fetch = [&](int c, int64_t at, int into) {
           const uint32_t dst = slots + (into & ahead) * piece_bytes + vec_off;
-          if (n < p.N && c + far * kSweep + tok < t.tokens) {
-            if (p.mul) ptx::copy16_async(dst, p.mul + at + far * step);
-            if (p.res) ptx::copy16_async(dst + res_off, p.res + at + far * step);
+          if (c < own) {
+            if (p.mul) ptx::copy16_async(dst, p.mul + at);
+            if (p.res) ptx::copy16_async(dst + res_off, p.res + at);
           }
           ptx::copy_commit();
         };
@@ -711,10 +701,10 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
         uchar2 sx = scales_of(c);
         __syncwarp();      // the tile before is read
         if (operands)
-          for (int far = 0; far < ahead; ++far) fetch(far, far);
+          for (int far = 0; far < ahead; ++far) fetch(c + far * kSweep, at + far * step, far);
+        const int64_t far = ahead * step;
         if (!wait_all(bar(kAccFull + b), (uint32_t)((u >> 1) & 1))) { give_up(); break; }
         ptx::tc_fence_after();
-        if (i + pairs < tiles) prefetch(after);      // its main loop is beginning
 #pragma unroll 1
         for (; c < t.tokens; c += kSweep, at += step, ++k) {
           float v[8];      // feature lane / 4 + 8 m, tokens c + 2 (lane % 4) + {0, 1}: v[2 m ..]
@@ -725,7 +715,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
             if (both) ptx::copy_wait<kSlots / 2 - 2>();
             else ptx::copy_wait<kSlots - 2>();
             __syncwarp();      // and every lane has read the results from the place that is filled next
-            fetch(ahead, k + ahead);
+            fetch(c + ahead * kSweep, at + far, k + ahead);
           }
           const uchar2 next = scales_of(c + kSweep);
           ptx::tmem_wait_ld();
@@ -759,7 +749,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
           if (operands) __syncwarp();      // the operand is read: its place takes the results
           ptx::stmatrix_x4_trans(piece + mat_off, w);
           __syncwarp();
-          if (n < p.N && c + tok < t.tokens) *reinterpret_cast<uint4*>(p.out + at) = ptx::ld_shared_v4(piece + vec_off);
+          if (c < own) *reinterpret_cast<uint4*>(p.out + at) = ptx::ld_shared_v4(piece + vec_off);
         }
       } else {
         if (F8) {
