@@ -658,8 +658,18 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     const uint32_t piece_bytes = both ? 2 * kSlotBytes : kSlotBytes, res_off = both ? kSlotBytes : 0;
     auto place = [](int token, int piece) { return (uint32_t)(64 * token + 16 * (piece ^ (token / 2 % 4))); };
     const uint32_t vec_off = place(lane / 4, lane % 4), mat_off = place(lane % 8, lane / 8);
+    // WIDE: scale bytes of the tokens of the warp's piece lane / 4 whose sums lane % 4 has, two each
+    auto scales_of = [&](const Tile& t) {
+      static_assert(!WIDE || 256 <= 8 * kEpiSets * kOctTokens, "a lane per two tokens");
+      const int j = kOctTokens * (set + kEpiSets * (lane / 4)) + 2 * (lane % 4);
+      uint32_t two = 0;
+      if (j < t.tokens) two = p.xs[t.t0 + j];
+      if (j + 1 < t.tokens) two |= (uint32_t)p.xs[t.t0 + j + 1] << 8;
+      return two;
+    };
     int u = 0;
     Tile t = tile_at(min(pair, tiles - 1)), after = t;
+    uint32_t scales_after = WIDE && F8 ? scales_of(t) : 0;
     prefetch(t);
     for (int i = pair; i < tiles; i += pairs, ++u) {
       const int b = u & 1;
@@ -690,15 +700,8 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
           }
           ptx::copy_commit();
         };
-        // scale bytes of the two tokens of a piece whose values this thread has
-        auto scales_of = [&](int c) {
-          const int j = c + 2 * (lane % 4);
-          uchar2 two = make_uchar2(0, 0);
-          if (F8 && j < t.tokens) two.x = p.xs[t.t0 + j];
-          if (F8 && j + 1 < t.tokens) two.y = p.xs[t.t0 + j + 1];
-          return two;
-        };
-        uchar2 sx = scales_of(c);
+        const uint32_t scales = scales_after;      // of this tile
+        if (F8 && i + pairs < tiles) scales_after = scales_of(after);
         __syncwarp();      // the tile before is read
         if (operands)
           for (int far = 0; far < ahead; ++far) fetch(c + far * kSweep, at + far * step, far);
@@ -717,16 +720,15 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
             __syncwarp();      // and every lane has read the results from the place that is filled next
             fetch(c + ahead * kSweep, at + far, k + ahead);
           }
-          const uchar2 next = scales_of(c + kSweep);
+          const uint32_t sx = F8 ? __shfl_sync(0xffffffffu, scales, 4 * k + lane % 4) : 0;
+          const ptx::F2 x = ptx::f2(scale_of((uint8_t)sx), scale_of((uint8_t)(sx >> 8)));
           ptx::tmem_wait_ld();
-          const ptx::F2 x = ptx::f2(scale_of(sx.x), scale_of(sx.y));
 #pragma unroll
           for (int m = 0; m < 4; ++m) {
             ptx::F2 two = ptx::f2(v[2 * m], v[2 * m + 1]);
             if (F8) two = ptx::mul2(ptx::mul2(two, ptx::f2(ws[m], ws[m])), x);
             ptx::split(ptx::add2(two, ptx::f2(bias[m], bias[m])), v[2 * m], v[2 * m + 1]);
           }
-          sx = next;
           activate(v, p.act);
           uint32_t w[4];
           if (p.mul) {
