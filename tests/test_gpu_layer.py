@@ -368,6 +368,62 @@ def test_linear_in_place_on_its_residual_and_on_mul(T, N, K):
     assert torch.equal(a, want) and torch.equal(b, want)
 
 
+# many tokens and rows of whole 16-byte pieces: features that end inside a warp's 32, tokens that end
+# inside a piece of 8 and a sweep of 32, tiles for every pair of SMs and more
+WIDE_SHAPES = [(2049, 8, 16), (2060, 40, 64), (2500, 304, 272), (3007, 136, 1008), (4101, 2568, 64), (5001, 1304, 144)]
+
+
+@pytest.mark.parametrize("operands", ["bare", "bias", "mul", "res", "mul res", "bias mul res"])
+@pytest.mark.parametrize("eight", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("T,N,K", WIDE_SHAPES)
+def test_linear_of_many_tokens_is_exact_with_any_operands(T, N, K, eight, operands):
+    rng = np.random.default_rng(T + 31 * N + K)
+    x, W = ints(rng, -4, 4, T, K), ints(rng, -3, 3, N, K)
+    bias = ints(rng, -9, 9, N) if "bias" in operands else None
+    mul = ints(rng, -3, 3, T, N) if "mul" in operands else None
+    res = ints(rng, -99, 99, T, N) if "res" in operands else None
+    dev = lambda a: None if a is None else bf16(a)  # noqa: E731
+    scales = None
+    tx, tw = bf16(x), bf16(W)
+    if eight:
+        kx, kw = rng.integers(-3, 4, size=T), rng.integers(-3, 4, size=N)
+        tx, tw = (torch.from_numpy(fp8.e4m3_encode(a)).to(DEV) for a in (x, W))
+        scales = tuple(torch.from_numpy((k + 127).astype(np.uint8)).to(DEV) for k in (kx, kw))
+        x, W = np.ldexp(x, kx[:, None]), np.ldexp(W, kw[:, None])
+    want = orc.round_bf16(layer.linear(x, W, bias, mul, res))      # exact in fp32, as above
+    got = run_linear(tx, tw, dev(bias), dev(mul), dev(res), T, N, K, scales=scales)
+    assert np.array_equal(host(got), want), f"{np.sum(host(got) != want)} of {want.size} differ"
+    for into in ("mul", "res"):      # out is the operand's own buffer
+        if into in operands:
+            m, r = dev(mul), dev(res)
+            out = m if into == "mul" else r
+            if eight:
+                mla.mla_linear_fp8(tx, scales[0], tw, scales[1], dev(bias), m, r, out, T, N, K, mla.MLA_ACT_NONE)
+            else:
+                mla.mla_linear(tx, tw, dev(bias), m, r, out, T, N, K, mla.MLA_ACT_NONE)
+            torch.cuda.synchronize()
+            assert np.array_equal(host(out), want), into
+
+
+@pytest.mark.parametrize("act", ["sigmoid", "silu", "gelu"])
+@pytest.mark.parametrize("N", [264, 259])
+def test_linear_of_many_tokens_applies_the_activation_to_the_sum(N, act):
+    """The same sums by themselves and in front of mul and residual, with 16-byte rows and without."""
+    rng = np.random.default_rng(N)
+    T, K = 2077, 64
+    x, W = rng.standard_normal((T, K)), rng.standard_normal((N, K)) / 4
+    xb, Wb = bf16(x), bf16(W)
+    bias, mul, res = bf16(rng.standard_normal(N)), bf16(rng.standard_normal((T, N))), bf16(rng.standard_normal((T, N)))
+    b, m, r = host(bias), host(mul), host(res)
+    x, W = host(xb), host(Wb)
+    got = run_linear(xb, Wb, bias, mul, res, T, N, K, act)
+    ref = layer.linear(x, W, b, m, r, act)
+    acc = (K + 2) * 2.0 ** -23 * (np.abs(x) @ np.abs(W).T + np.abs(b))
+    part = np.abs(m) * (1.13 * acc + 2.0 ** -20 * np.abs(layer.activation(x @ W.T + b, act)))
+    bound = 2.0 ** -8 * np.abs(ref) + (1 + 2.0 ** -8) * (part + 2.0 ** -22 * np.abs(r)) + 1e-30
+    assert np.all(np.abs(host(got) - ref) <= bound)
+
+
 @pytest.mark.parametrize("T,N,K", [(3, 140, 256), (260, 140, 256)])
 def test_linear_keeps_a_rows_nan_and_infinity_in_that_row(T, N, K):
     rng = np.random.default_rng(6)
