@@ -462,10 +462,23 @@ __global__ void __launch_bounds__(kSplitThreads, 2) linear_split_kernel(const __
 // ------------------------------------------------------------------ many tokens: SM pairs
 // p.nt tokens a tile (a multiple of 16, at most 256; two accumulators in TMEM), p.stages
 // stages. Warp 0 loads, warp 1 issues the MMAs (even CTA), warp 2 holds TMEM, warps 4.. run the
-// epilogue (two per 32 TMEM lanes, on alternate chunks of 16 tokens; a lane's accesses are its feature's, 64 bytes a warp and token, whatever N's
-// alignment). Where K is short the epilogue is what a tile takes: its instructions count.
-// (Turning the sums through shared memory into 16-byte accesses, with the operands brought by
-// TMA, was no faster: 4096 x 7168 x 512 with a residual and a sigmoid 67 against 58 us.)
+// epilogue. Where K is short (below ~1000 for a bare output, ~2000 with a gate and a residual, more for
+// gelu) the epilogue is what a tile takes: its instructions and its few warps' latencies
+// count. Two forms:
+//   WIDE, where N and the pointers let rows move in 16-byte parts: sixteen warps, each 32
+//   features and every fourth piece of 8 tokens. The sums are read in the matrix fragment's shape
+//   (16 lanes x 256 bits), two tokens of a feature side by side, so that paired fp32 instructions
+//   serve both and the transposing matrix store turns them into rows of shared memory; mul and
+//   residual come the other way, by the thread's asynchronous copies and the transposing matrix
+//   load.
+//   otherwise: eight warps, two per 32 TMEM lanes on alternate chunks of 16 tokens, a feature a
+//   lane: every access is 2 bytes a lane, 64 a warp and token, at any alignment.
+// (8192 x 8192 x 64 bf16, us, otherwise -> WIDE: bare 64 -> 41, with a residual 95 -> 72, with residual
+// and sigmoid 107 -> 79, gelu 143 -> 96, all of it and gelu 188 -> 132. Of that the wide accesses
+// with eight warps gave 49 / 86 / 102 / 123 / 162. 12 and 20 warps were slower, and so was asking
+// L2 for the next tile's operands, which the narrow form wants: 8192 x 8192 x 1024 with residual
+// and sigmoid 114 against 102. Eight slots a warp for one stage of the ring less: 67 us with a
+// residual, but 92 against 88 at K = 1024 bare.)
 __host__ __device__ constexpr int epi_warps(bool wide) { return wide ? 16 : 8; }
 __host__ __device__ constexpr int pair_threads(bool wide) { return 32 * (4 + epi_warps(wide)); }
 // Behind the ring, per epilogue warp: its tile's token scales (8-bit operands); in the WIDE kernel
@@ -643,15 +656,16 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive_cluster_relaxed(lead(bar(kAccFree + b)));
     };
-    // this warp's share of a tile's operands into L2, a tile ahead
+    // this warp's share of a tile's operands into L2, a tile ahead (not WIDE)
     auto prefetch = [&](const Tile& t) {
-      if (!WIDE && (p.mul || p.res)) prefetch_rows(p, t.t0, t.tokens, t.nw, 32, set, kEpiSets, lane);
+      if (p.mul || p.res) prefetch_rows(p, t.t0, t.tokens, t.nw, 32, set, kEpiSets, lane);
     };
     float* scale = reinterpret_cast<float*>(smem + off_epi) + (warp - 4) * 256;      // not WIDE
     // WIDE: a piece lies [token][feature] in its place, 64 bytes a token, whose 16-byte parts are
     // turned by the token so that neither access has a bank conflict: lane / 4 is the token and lane %
-    // 4 the part of the 16-byte accesses, lane % 8 and lane / 8 those of the matrix ones. With one
-    // operand three pieces are on their way behind the one at work, with two one.
+    // 4 the part of the 16-byte accesses, lane % 8 and lane / 8 those of the matrix ones. The results
+    // take the place of the piece's operand. With one operand three pieces are on their way behind
+    // the one at work, with two one.
     const uint32_t slots = sbase + off_epi + (warp - 4) * (kSlots * kSlotBytes);
     const bool operands = p.mul || p.res, both = p.mul && p.res;
     const int ahead = both ? kSlots / 2 - 1 : kSlots - 1;
@@ -670,7 +684,7 @@ linear_pair_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constan
     int u = 0;
     Tile t = tile_at(min(pair, tiles - 1)), after = t;
     uint32_t scales_after = WIDE && F8 ? scales_of(t) : 0;
-    prefetch(t);
+    if (!WIDE) prefetch(t);
     for (int i = pair; i < tiles; i += pairs, ++u) {
       const int b = u & 1;
       t = after;
