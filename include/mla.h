@@ -334,7 +334,8 @@ mla_status mla_prefill_attn(const void* ckr, const void* q_nope, const void* q_r
  * stream, the projections that make the queries, the optional output gate and Wo with the
  * residual's addition (kimi-k3 docs "GatedMLA", "Projection geometry and stored weights"
  * and "Output projection and optional gate"). All sums and statistics are fp32; each
- * output element is rounded once, where it is stored. Any sizes: no dims, no workspace.
+ * output element is rounded once, where it is stored. Any sizes, rows (M, width, K) of up to
+ * 0x7FFFF000 elements (longer ones: MLA_ERR_INVALID); no dims, no workspace.
  *
  * Residual addition and RMS norm of rows x [T][M]:
  *   s = x + residual (s = x without one),  residual_out = s,

@@ -1376,10 +1376,14 @@ bool overlap(const Span& a, const Span& b) {
 // writes it; it may not overlap an input in any other way.
 bool overlap_shifted(const Span& a, const Span& b) { return a.p != b.p && overlap(a, b); }
 
+// The longest row of the layer's operators: its kernels count a row's elements in 32 bits and
+// step by up to a block of threads, or round up to a K block, past the last one.
+constexpr int32_t kMaxRow = 0x7FFFF000;
+
 mla_status add_rmsnorm(const char* what, const void* x, const void* residual, const void* gain, void* residual_out,
                        void* out, void* codes, void* scales, int32_t T, int32_t M, float eps, int32_t dtype,
                        bool with_codes, void* stream) {
-  if (T < 0 || M <= 0) return fail(MLA_ERR_INVALID, "%s: bad sizes T=%d M=%d", what, T, M);
+  if (T < 0 || M <= 0 || M > kMaxRow) return fail(MLA_ERR_INVALID, "%s: bad sizes T=%d M=%d", what, T, M);
   if (dtype != MLA_BF16 && dtype != MLA_F32)
     return fail(MLA_ERR_INVALID, "%s: dtype must be MLA_BF16 or MLA_F32, got %d", what, dtype);
   if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(MLA_ERR_INVALID, "%s: eps must be finite and >= 0", what);
@@ -1545,7 +1549,8 @@ mla_status linear_tc(const void* x, const void* W, const mla::lin::Params& p, cu
 mla_status linear(const char* what, bool f8, const void* x, const void* xs, const void* W, const void* ws,
                   const void* bias, const void* mul, const void* residual, void* out, int32_t T, int32_t N, int32_t K,
                   int32_t act, void* stream) {
-  if (T < 0 || N <= 0 || K <= 0) return fail(MLA_ERR_INVALID, "%s: bad sizes T=%d N=%d K=%d", what, T, N, K);
+  if (T < 0 || N <= 0 || K <= 0 || K > kMaxRow)
+    return fail(MLA_ERR_INVALID, "%s: bad sizes T=%d N=%d K=%d", what, T, N, K);
   if (act < MLA_ACT_NONE || act > MLA_ACT_GELU) return fail(MLA_ERR_INVALID, "%s: unknown activation %d", what, act);
   if (T == 0) return ok();
   if (!x || !W || !out || (f8 && (!xs || !ws))) return fail(MLA_ERR_INVALID, "%s: null pointer", what);
@@ -1609,7 +1614,8 @@ mla_status mla_add_rmsnorm_fp8(const void* x, const void* residual, const void* 
 
 mla_status mla_quantize_fp8(const void* rows, void* codes, void* scales, int32_t n, int32_t width, int32_t dtype,
                             void* stream) {
-  if (n < 0 || width <= 0) return fail(MLA_ERR_INVALID, "quantize_fp8: bad sizes n=%d width=%d", n, width);
+  if (n < 0 || width <= 0 || width > kMaxRow)
+    return fail(MLA_ERR_INVALID, "quantize_fp8: bad sizes n=%d width=%d", n, width);
   if (dtype != MLA_BF16 && dtype != MLA_F32)
     return fail(MLA_ERR_INVALID, "quantize_fp8: dtype must be MLA_BF16 or MLA_F32, got %d", dtype);
   if (n == 0) return ok();
