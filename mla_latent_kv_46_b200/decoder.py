@@ -162,7 +162,10 @@ class LayerStep:
     [H*Dv, M] (each out x in). projections="fp8": the query, gate and output projections
     run in 8 bits, their weights quantised here once (finished on return, so that any stream
     may run the step); the cache write keeps bf16 rows. The step's tensors and its cache must be
-    bf16. One run of an object at a time: its buffers are the step's."""
+    bf16. One run of an object at a time: its buffers are the step's.
+
+    A first layer, or one whose input already is the residual stream (another layer's y), runs
+    with residual=None: the stream is then x itself, which is read until the run's end."""
 
     def __init__(self, step: DecodeStep, weights: dict, projections: str = "bf16", eps: float = 1e-6,
                  rope_base: float = 10000.0):
@@ -197,6 +200,7 @@ class LayerStep:
         self.residual = empty(self.T, self.M)     # the stream after the addition
         self.hidden = empty(self.T, self.M)       # its normalised rows
         self.y = empty(self.T, self.M)            # the stream after the layer
+        self.trunk = self.residual               # the rows that Wo's result is added to
         self.ws_bytes = mla.mla_cache_write_workspace_size(self.T, self.M)
         self.workspace = empty(max(self.ws_bytes, 16), dtype=torch.uint8)
         if self.fp8:
@@ -219,6 +223,16 @@ class LayerStep:
         if not x.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
 
+    def _refuse_own_buffer(self, x):
+        """x is the trunk until Wo: not a buffer that the run writes before."""
+        st = self.step
+        written = [self.hidden, self.workspace, st.q_nope, st.q_rope, st.q_lat, st.o_lat, st.lse, st.out, st.workspace,
+                   st.kv] + ([self.codes, self.scales, self.out_codes, self.out_scales] if self.fp8 else [])
+        lo, hi = x.data_ptr(), x.data_ptr() + x.numel() * x.element_size()
+        if any(lo < b.data_ptr() + b.numel() * b.element_size() and b.data_ptr() < hi for b in written):
+            raise ValueError("x without a residual is read until the run's end: it cannot be a buffer that the run "
+                             "writes before")
+
     def _project(self, name, out, n, act=mla.MLA_ACT_NONE, mul=None, stream=None):
         """out = mul * act(hidden W^T)."""
         if self.fp8:
@@ -228,16 +242,21 @@ class LayerStep:
             mla.mla_linear(self.hidden, self.w[name], None, mul, None, out, self.T, n, self.M, act, stream)
 
     def norm_and_queries(self, x, residual, stream=None):
-        """residual + x and its normalised rows, and the step's queries from them."""
+        """residual + x (x without a residual) and its normalised rows, and the step's queries
+        from them."""
         st = self.step
         self._expect(x, (self.T, self.M), "x")
         if residual is not None:
             self._expect(residual, (self.T, self.M), "residual")
+            self.trunk, stored = self.residual, self.residual
+        else:
+            self._refuse_own_buffer(x)
+            self.trunk, stored = x, None
         if self.fp8:
-            mla.mla_add_rmsnorm_fp8(x, residual, self.w["gain"], self.residual, self.hidden, self.codes, self.scales,
+            mla.mla_add_rmsnorm_fp8(x, residual, self.w["gain"], stored, self.hidden, self.codes, self.scales,
                                     self.T, self.M, self.eps, mla.MLA_BF16, stream)
         else:
-            mla.mla_add_rmsnorm(x, residual, self.w["gain"], self.residual, self.hidden, self.T, self.M, self.eps,
+            mla.mla_add_rmsnorm(x, residual, self.w["gain"], stored, self.hidden, self.T, self.M, self.eps,
                                 mla.MLA_BF16, stream)
         self._project("W_QN", st.q_nope, self.n_nope, stream=stream)
         self._project("W_QR", st.q_rope, self.n_rope, stream=stream)
@@ -249,21 +268,21 @@ class LayerStep:
                             self.rope_base, self.workspace, self.ws_bytes, st.dims, stream)
 
     def gate_and_output(self, stream=None):
-        """y = residual + Wo(gate * attention)."""
+        """y = trunk + Wo(gate * attention)."""
         st = self.step
         if self.gated:
             self._project("W_G", st.out, self.n_out, mla.MLA_ACT_SIGMOID, st.out, stream)     # in place
         if self.fp8:
             mla.mla_quantize_fp8(st.out, self.out_codes, self.out_scales, self.T, self.n_out, mla.MLA_BF16, stream)
-            mla.mla_linear_fp8(self.out_codes, self.out_scales, *self.w8["W_O"], None, None, self.residual, self.y,
+            mla.mla_linear_fp8(self.out_codes, self.out_scales, *self.w8["W_O"], None, None, self.trunk, self.y,
                                self.T, self.M, self.n_out, mla.MLA_ACT_NONE, stream)
         else:
-            mla.mla_linear(st.out, self.w["W_O"], None, None, self.residual, self.y, self.T, self.M, self.n_out,
+            mla.mla_linear(st.out, self.w["W_O"], None, None, self.trunk, self.y, self.T, self.M, self.n_out,
                            mla.MLA_ACT_NONE, stream)
 
     def run(self, x, residual, stream=None):
-        """The whole step for the new tokens' layer input x and residual stream [T, M];
-        returns y [T, M], the residual stream after the layer (this object's buffer)."""
+        """The whole step for the new tokens' layer input x and residual stream [T, M] (None: x is
+        the stream); returns y [T, M], the residual stream after the layer (this object's buffer)."""
         self.norm_and_queries(x, residual, stream)
         self.cache_write(stream)
         self.step.run(append=False, stream=stream)
