@@ -441,9 +441,13 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_any_kernel(const Params p) {
   const T* x = static_cast<const T*>(p.x) + at;
   const T* r = p.r ? static_cast<const T*>(p.r) + at : nullptr;
   const T* g = static_cast<const T*>(p.gain);
+  auto sum = [&](int c) {      // (not x + 0 without r: that would lose the sign of -0)
+    const float v = to_f32<T>(x[c]);
+    return r ? v + to_f32<T>(r[c]) : v;
+  };
   float ss = 0.f, am = 0.f;
   for (int c = threadIdx.x; c < p.M; c += blockDim.x) {
-    const float s = to_f32<T>(x[c]) + (r ? to_f32<T>(r[c]) : 0.f);
+    const float s = sum(c);
     ss += s * s;
     am = fmaxf(am, fabsf(g ? s * to_f32<T>(g[c]) : s));
   }
@@ -452,7 +456,7 @@ __global__ void __launch_bounds__(1024) add_rmsnorm_any_kernel(const Params p) {
   const int k = scale_exponent(am * inv);
   const float up = f8::pow2(-k);
   for (int c = threadIdx.x; c < p.M; c += blockDim.x) {
-    const float s = to_f32<T>(x[c]) + (r ? to_f32<T>(r[c]) : 0.f);
+    const float s = sum(c);
     if (p.r_out) static_cast<T*>(p.r_out)[at + c] = from_f32<T>(s);
     const float y = g ? (s * to_f32<T>(g[c])) * inv : s;
     if (p.y) static_cast<T*>(p.y)[at + c] = from_f32<T>(y);
