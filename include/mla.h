@@ -352,7 +352,8 @@ mla_status mla_add_rmsnorm(const void* x, const void* residual, const void* gain
  * 8-bit cache above (E4M3 codes of the fp32 result, one power-of-two scale byte per row;
  * rounded once, from fp32). `out` (dtype) may be NULL, or is written beside the codes, for
  * a layer whose cache write takes bf16 rows and whose projections take 8-bit ones. A NaN
- * gets the NaN code 0x7F or 0xFF and does not count towards its row's scale.             */
+ * gets the NaN code 0x7F or 0xFF and does not count towards its row's scale: a row of NaNs, or of
+ * NaNs and zeros, has the smallest one.                                                  */
 mla_status mla_add_rmsnorm_fp8(const void* x, const void* residual, const void* gain, void* residual_out, void* out,
                                void* codes, void* scales, int32_t T, int32_t M, float eps, int32_t dtype,
                                void* stream);

@@ -48,9 +48,10 @@ template <typename T> __host__ __device__ constexpr int granule() { return 16 / 
 // The scale exponent of a row whose largest magnitude is amax: the smallest k in
 // [-126, 7] with amax <= 448 2^k. 448 = 1.75 * 2^8, so an amax of mantissa up to 1.75
 // takes its own exponent - 8, a larger one exponent - 7. An infinite amax gives 7, a zero
-// or subnormal one -126.
+// or subnormal one -126. So does a NaN, max |s g| times a 1 / sqrt that is NaN, or infinity
+// times zero either way round: then every value of the row is a NaN, which does not count, or 0.
 __device__ __forceinline__ int scale_exponent(float amax) {
-  const uint32_t u = __float_as_uint(amax);
+  const uint32_t u = __float_as_uint(fmaxf(amax, 0.f));
   const int e = (int)(u >> 23) - 127;
   const int k = (u & 0x7FFFFFu) <= 0x600000u ? e - 8 : e - 7;
   return min(max(k, f8::kKMin), f8::kKMax);
