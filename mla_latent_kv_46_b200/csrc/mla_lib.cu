@@ -56,11 +56,15 @@ mla_status ok() {
   return MLA_OK;
 }
 
+// (The runtime also keeps the error for cudaGetLastError: taken from it here, or the next call's
+// launch check would report it again.)
 #define MLA_CUDA_TRY(expr)                                                               \
   do {                                                                                   \
     cudaError_t e_ = (expr);                                                             \
-    if (e_ != cudaSuccess)                                                               \
+    if (e_ != cudaSuccess) {                                                             \
+      (void)cudaGetLastError();                                                          \
       return fail(MLA_ERR_CUDA, "%s failed: %s", #expr, cudaGetErrorString(e_));          \
+    }                                                                                    \
   } while (0)
 
 mla_status check_dims(const mla_dims& d) {
@@ -1246,8 +1250,10 @@ namespace {
 int32_t device_sms() {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    (void)cudaGetLastError();      // as in MLA_CUDA_TRY
     return 0;
+  }
   return sms;
 }
 
@@ -1294,7 +1300,10 @@ int blocks_per_sm(const void* kernel, int threads, int64_t smem) {
     if (k.kernel == kernel && k.threads == threads && k.smem == smem && k.dev == dev) return k.blocks;
   }
   int blocks = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, threads, (size_t)smem) != cudaSuccess) return 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, threads, (size_t)smem) != cudaSuccess) {
+    (void)cudaGetLastError();      // as in MLA_CUDA_TRY
+    return 0;
+  }
   known[next] = Known{kernel, threads, dev, blocks, smem};
   next = (next + 1) % kKept;
   kept = std::max(kept, next == 0 ? kKept : next);
