@@ -117,11 +117,15 @@ _cuda = None   # torch._C once a call needed it: (current device, its current st
 
 def _cuda_calls():
     """torch's current-device and current-stream lookups without their Python wrappers (a call's
-    host time is a few microseconds: a Stream object alone takes 3, a repeated import 0.1)."""
+    host time is a few microseconds: a Stream object alone takes 3, a repeated import 0.1); those
+    names are torch's own, and the public wrappers serve where they are missing."""
     global _cuda
     import torch
     torch.cuda.current_device()      # initialises CUDA
-    _cuda = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+    try:
+        _cuda = (torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream)
+    except AttributeError:
+        _cuda = (torch.cuda.current_device, lambda device: torch.cuda.current_stream(device).cuda_stream)
     return _cuda
 
 
