@@ -387,6 +387,14 @@ mla_status mla_linear_fp8(const void* x_codes, const void* x_scales, const void*
                           const void* bias, const void* mul, const void* residual, void* out, int32_t T, int32_t N,
                           int32_t K, int32_t act, void* stream);
 
+/* TEST-ONLY: which tensor-core kernel mla_linear (eight_bit = 0) or mla_linear_fp8 takes for these
+ * sizes with `operands` of mul and residual given (0 .. 2), on a device of `sms` SMs whose clusters
+ * hold up to max_slices K slices of two CTAs (1, 2, 4 or 8); sms <= 0: on the current device. Host
+ * only. choice_host[4]: 1 if it is the persistent many-token kernel (0: the few-token one), tokens
+ * per tile, K slices, CTAs per SM. Nothing in the pages corresponds to it.               */
+mla_status mla_debug_linear_choice(int32_t T, int32_t N, int32_t K, int32_t eight_bit, int32_t operands, int32_t sms,
+                                   int32_t max_slices, int32_t* choice_host);
+
 /* ---------------------------------------------------------------- allocation-free decode
  * The pages describe no counterpart of this call; it exists for callers that cannot
  * allocate device memory: code inside another framework's fixed memory pool, or a

@@ -30,7 +30,7 @@ EXPORTS = ("mla_abi_version", "mla_last_error", "mla_set_policy", "mla_set_wait_
            "mla_workspace_size", "mla_decode_attn", "mla_combine", "mla_out_proj", "mla_decode_attn_noalloc",
            "mla_debug_drop_page_load", "mla_quantize_rows_fp8", "mla_cache_append_fp8", "mla_workspace_size_fp8",
            "mla_decode_attn_fp8", "mla_prefill_workspace_size", "mla_prefill_attn", "mla_add_rmsnorm", "mla_add_rmsnorm_fp8",
-           "mla_quantize_fp8", "mla_linear", "mla_linear_fp8")
+           "mla_quantize_fp8", "mla_linear", "mla_linear_fp8", "mla_debug_linear_choice")
 
 
 class MlaError(RuntimeError):
@@ -90,6 +90,7 @@ def _load():
         "mla_add_rmsnorm_fp8": (I32, [P, P, P, P, P, P, P, I32, I32, F, I32, P]),
         "mla_quantize_fp8": (I32, [P, P, P, I32, I32, I32, P]),
         "mla_linear": (I32, [P, P, P, P, P, P, I32, I32, I32, I32, P]),
+        "mla_debug_linear_choice": (I32, [I32, I32, I32, I32, I32, I32, I32, P]),
         "mla_linear_fp8": (I32, [P, P, P, P, P, P, P, P, I32, I32, I32, I32, P]),
     }
     for name, (res, args) in sig.items():
@@ -320,3 +321,11 @@ def mla_linear(x, W, bias, mul, residual, out, T, N, K, act, stream=None):
 def mla_linear_fp8(x_codes, x_scales, W_codes, W_scales, bias, mul, residual, out, T, N, K, act, stream=None):
     _check(_lib.mla_linear_fp8(*_dense(x_codes, x_scales, W_codes, W_scales, bias, mul, residual, out), T, N, K, act,
                                _stream(stream)), "mla_linear_fp8")
+
+
+def mla_debug_linear_choice(T, N, K, eight_bit, operands=0, sms=0, max_slices=0):
+    """(many-token kernel?, tokens per tile, K slices, CTAs per SM) of a projection; testing aid."""
+    choice = (ctypes.c_int32 * 4)()
+    _check(_lib.mla_debug_linear_choice(T, N, K, int(eight_bit), operands, sms, max_slices, ctypes.addressof(choice)),
+           "mla_debug_linear_choice")
+    return bool(choice[0]), choice[1], choice[2], choice[3]

@@ -1451,6 +1451,55 @@ mla_status linear_maps(CUtensorMap* tw, CUtensorMap* tx, const void* W, const vo
 // Shared memory a block may have where an SM is to hold two (each takes 1 KiB more), or one.
 constexpr int kSmemOfTwo = 113 * 1024, kSmemOfOne = 226 * 1024;
 
+// The few-token kernel has two CTAs an SM where there are that many and they fit; else one,
+// with all of its memory.
+bool two_an_sm(int nt, int slices, double tiles, int sms) {
+  return 2 * slices * tiles > sms && mla::lin::split_smem(nt, 2, slices) <= kSmemOfTwo;
+}
+
+// The most K slices the current device can run: a slice is a pair of a cluster's CTAs, each with
+// an SM's shared memory, and a cluster's SMs are one GPC's. (B200s hold 16 to 20 SMs a GPC and take
+// all eight slices; parts of a GPU may not.) Asked for once per operand type and device; sets the
+// kernel's attributes on the way.
+template <bool F8>
+mla_status most_slices(int* slices) {
+  using namespace mla::lin;
+  static std::mutex mu;
+  static std::vector<std::pair<int, int>> known;   // (device, slices)
+  auto kern = linear_split_kernel<F8>;
+  if (mla_status s = ensure_smem_attr((const void*)kern, kSmemOfOne)) return s;
+  int dev = 0;
+  MLA_CUDA_TRY(cudaGetDevice(&dev));
+  std::lock_guard<std::mutex> lk(mu);
+  for (auto& e : known)
+    if (e.first == dev) {
+      *slices = e.second;
+      return MLA_OK;
+    }
+  // (clusters of more than eight CTAs are above the portable size)
+  MLA_CUDA_TRY(cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
+  for (*slices = kMaxSlices; *slices > 1; *slices /= 2) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * (unsigned)*slices);
+    cfg.blockDim = dim3(kSplitThreads);
+    cfg.dynamicSmemBytes = (size_t)kSmemOfOne;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2 * (unsigned)*slices;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if (cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg) != cudaSuccess) {
+      (void)cudaGetLastError();      // as in MLA_CUDA_TRY
+      clusters = 0;
+    }
+    if (clusters > 0) break;
+  }
+  known.emplace_back(dev, *slices);
+  return MLA_OK;
+}
+
 template <bool F8>
 mla_status launch_linear_split(const void* x, const void* W, mla::lin::Params p, int nt, int slices, int32_t sms,
                                cudaStream_t st, const char* what) {
@@ -1458,12 +1507,8 @@ mla_status launch_linear_split(const void* x, const void* W, mla::lin::Params p,
   auto kern = linear_split_kernel<F8>;
   CUtensorMap tw, tx;
   if (mla_status s = linear_maps<F8>(&tw, &tx, W, x, p, kM, (uint32_t)nt / 2)) return s;
-  if (mla_status s = ensure_smem_attr((const void*)kern, kSmemOfOne)) return s;
-  if (2 * slices > 8)   // above the portable cluster size
-    MLA_CUDA_TRY(cudaFuncSetAttribute((const void*)kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1));
   const int64_t tiles_n = ((int64_t)p.N + 2 * kM - 1) / (2 * kM), tiles_t = ((int64_t)p.T + nt - 1) / nt;
-  // two CTAs an SM where there are that many and they fit; else one, with all of its memory
-  const bool two = 2 * slices * tiles_n * tiles_t > sms && split_smem(nt, 2, slices) <= kSmemOfTwo;
+  const bool two = two_an_sm(nt, slices, tiles_n * tiles_t, sms);
   p.nt = nt;
   p.stages = std::min(kMaxStages, ((two ? kSmemOfTwo : kSmemOfOne) - kSmemSlack) / stage_bytes_of(nt));
   return launch_overlapped(what, kern, dim3(2 * (unsigned)slices, (unsigned)tiles_n, (unsigned)tiles_t), kSplitThreads,
@@ -1497,7 +1542,7 @@ struct LinearChoice {
   bool pair;      // the persistent kernel
   int nt, slices;
 };
-LinearChoice choose_linear(const mla::lin::Params& p, bool f8, int sms) {
+LinearChoice choose_linear(const mla::lin::Params& p, bool f8, int sms, int max_slices) {
   using namespace mla::lin;
   const int kblk = (int)(((int64_t)p.K * (f8 ? 1 : 2) + kKBytes - 1) / kKBytes);
   const int64_t tiles_n = ((int64_t)p.N + 2 * kM - 1) / (2 * kM);
@@ -1528,11 +1573,11 @@ LinearChoice choose_linear(const mla::lin::Params& p, bool f8, int sms) {
       const int nt = up16((p.T + j - 1) / j);
       if (nt > 256 || (j > 1 && nt < 32)) continue;
       const double tiles = tiles_n * std::ceil((double)p.T / nt);
-      for (int slices = 1; slices <= kMaxSlices; slices *= 2) {
+      for (int slices = 1; slices <= max_slices; slices *= 2) {
         if (slices > 1 && 2 * slices > kblk) break;
         // clusters of 2 * slices CTAs that fit at once, at one CTA an SM: GPCs hold 16 to 20 SMs
         const int fit = slices == 1 ? (int)pairs : slices == 2 ? 36 : slices == 4 ? 14 : 7;
-        const bool two = 2 * slices * tiles > sms && split_smem(nt, 2, slices) <= kSmemOfTwo;
+        const bool two = two_an_sm(nt, slices, tiles, sms);
         if (slices == kMaxSlices && tiles > fit) break;
         if (split_smem(nt, 1, slices) > kSmemOfOne) continue;
         const double waves = std::ceil(tiles / (fit * (two ? 2 : 1)));
@@ -1548,7 +1593,9 @@ LinearChoice choose_linear(const mla::lin::Params& p, bool f8, int sms) {
 template <bool F8>
 mla_status linear_tc(const void* x, const void* W, const mla::lin::Params& p, cudaStream_t st, const char* what) {
   const int32_t sms = device_sms();
-  const LinearChoice c = choose_linear(p, F8, sms);
+  int slices = 1;
+  if (mla_status s = most_slices<F8>(&slices)) return s;
+  const LinearChoice c = choose_linear(p, F8, sms, slices);
   if (c.pair)
     return p.octs ? launch_linear_pair<F8, true>(x, W, p, c.nt, sms, st, what)
                   : launch_linear_pair<F8, false>(x, W, p, c.nt, sms, st, what);
@@ -1642,6 +1689,32 @@ mla_status mla_quantize_fp8(const void* rows, void* codes, void* scales, int32_t
   p.T = n;
   p.M = width;
   return dtype == MLA_BF16 ? launch_rms<__nv_bfloat16>(p, as_stream(stream)) : launch_rms<float>(p, as_stream(stream));
+}
+
+mla_status mla_debug_linear_choice(int32_t T, int32_t N, int32_t K, int32_t eight_bit, int32_t operands, int32_t sms,
+                                   int32_t max_slices, int32_t* choice_host) {
+  if (T <= 0 || N <= 0 || K <= 0 || K > kMaxRow || operands < 0 || operands > 2 || !choice_host)
+    return fail(MLA_ERR_INVALID, "debug_linear_choice: bad arguments T=%d N=%d K=%d operands=%d", T, N, K, operands);
+  if (sms <= 0) {
+    sms = device_sms();
+    int slices = 1;
+    if (mla_status s = eight_bit ? most_slices<true>(&slices) : most_slices<false>(&slices)) return s;
+    max_slices = slices;
+  }
+  mla::lin::Params p{};
+  const __nv_bfloat16 given{};      // (the choice looks at which operands there are, not at them)
+  p.mul = operands > 0 ? &given : nullptr;
+  p.res = operands > 1 ? &given : nullptr;
+  p.T = T;
+  p.N = N;
+  p.K = K;
+  const LinearChoice c = choose_linear(p, eight_bit != 0, sms, max_slices);
+  const int64_t tiles_n = ((int64_t)N + 2 * mla::lin::kM - 1) / (2 * mla::lin::kM), tiles_t = ((int64_t)T + c.nt - 1) / c.nt;
+  choice_host[0] = c.pair;
+  choice_host[1] = c.nt;
+  choice_host[2] = c.slices;
+  choice_host[3] = !c.pair && two_an_sm(c.nt, c.slices, (double)(tiles_n * tiles_t), sms) ? 2 : 1;
+  return ok();
 }
 
 mla_status mla_linear(const void* x, const void* W, const void* bias, const void* mul, const void* residual, void* out,
