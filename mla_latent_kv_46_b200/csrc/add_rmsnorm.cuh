@@ -17,8 +17,8 @@
 // granule tM / VE. x, r, r' and y share that layout; the codes of a granule are VE aligned
 // bytes, for tM - shift is a multiple of VE. A row's first and last granule may hold a
 // neighbour's elements: those are read and ignored, and never written. Only the gain is
-// out of step with a shifted row. (16384 x 1111 bf16: 33 us; with 2-byte accesses instead,
-// as the row's own alignment allows, about 100.)
+// out of step with a shifted row. (16384 x 1111 bf16: 31 us with a residual, 26 without; with
+// 2-byte accesses instead, as the row's own alignment allows, about 100.)
 #pragma once
 
 #include "common.cuh"
@@ -243,7 +243,8 @@ __device__ __forceinline__ void second_step(const Params& p, const Row<granule<T
 // as many threads as the row has granules a call of a few rows is one round trip to memory,
 // and a thread's loads are all in flight before the first is used. One row a block: blocks
 // that stay and load the next row's granules under this row's exchange were slower (16384 x
-// 1111 bf16 45 against 37 us; 8000 x 1112 fp32 17.5 against 14.8). A thread keeps its
+// 1111 bf16 45 us against 37 for this kernel's form of then, which now takes 31; 8000 x 1112 fp32
+// 17.5 against 14.8). A thread keeps its
 // elements and their gains, so blocks of 1024 threads hold up to 16 elements a thread, and
 // kWideThreads up to 32.
 constexpr int kWideThreads = 544;   // 16384 elements and a shifted row's one granule more
@@ -315,7 +316,9 @@ add_rmsnorm_kernel(const Params p) {
 // shared memory that bulk copies keep full while the block works on the oldest row. ITEMS
 // granules a thread, whose gains it keeps for every row. One barrier per row: once it has
 // passed, every thread holds its part of the row in registers and the buffer is loaded
-// again. The inputs are read once, so they are loaded with evict-first priority, which
+// again. It is not instantiated for the quantiser, which has a block a row (16384 x 8192
+// bf16: 114 us, 61 for the bytes). The inputs are read
+// once, so they are loaded with evict-first priority, which
 // leaves L2 to the writes (T = 16384, M = 7168, bf16 with a residual: 155 us, 6.05 TB/s,
 // against 169 us without, and 204 for the kernel above; two buffers and four granules a
 // thread beat three buffers, or two or eight granules). Shifted rows gained nothing here.
@@ -432,7 +435,9 @@ __global__ void __launch_bounds__(kStreamThreads) add_rmsnorm_stream_kernel(cons
 // Any width and alignment: one block per row, two passes over it (the second reads again
 // what the first summed; r_out and y are written in the second, element by element by the
 // thread that read them, so they may be r's and x's own buffers). For operands that are not
-// 16-byte aligned, and rows too wide for the registers of a block.
+// 16-byte aligned, and rows too wide for the registers of a block (above 17,408 elements).
+// Element by element and twice over the row: 2048 x 18432 bf16 with a residual 131 us, where
+// 2048 x 16384 takes 47; 2048 x 7168 one element off 56 us, aligned 21.
 template <typename T>
 __global__ void __launch_bounds__(1024) add_rmsnorm_any_kernel(const Params p) {
   __shared__ float red[2][32];

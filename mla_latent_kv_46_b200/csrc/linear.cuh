@@ -5,7 +5,9 @@
 // Sums are fp32; bias, activation, mul and residual are applied to the fp32 sum and the
 // result is rounded once, to bf16. 8-bit operands are E4M3 codes with one power-of-two
 // scale per row of x and of W (see fp8_kernels.cuh): the codes' products are summed and the
-// two scales multiply the sum, exactly.
+// two scales multiply the sum, W's first: exact, but where that first product is subnormal (below
+// 2^-126) and off by up to 2^-150, 2^-143 behind x's scale of at most 2^7: half a step of a bf16
+// result is 2^-134 there or more.
 #pragma once
 
 #include "common.cuh"
@@ -34,8 +36,9 @@ struct Params {
 __device__ __forceinline__ float scale_of(uint8_t b) { return __uint_as_float((uint32_t)b << 23); }
 
 // exp by ex2.approx and the quotient by rcp.approx, a few units in 2^-22 off (the result is
-// rounded to bf16, 2^-9): a full division took a third of the epilogue's instructions. Sums so
-// negative that e^-v overflows give 0, as the formulas do.
+// rounded to bf16, 2^-9): a full division took a third of the epilogue's instructions. The quotient
+// is 0 once 1 + e^-v passes 2^126, for sums below about -87.3, where sigmoid is below 1.2e-38 and silu
+// below 1.1e-36 in magnitude (in fp32 the formulas give 0 from -88.7 on, where e^-v overflows).
 __device__ __forceinline__ float sigmoid(float v) { return __fdividef(1.f, 1.f + __expf(-v)); }
 __device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.f + __expf(-v)); }
 // v Phi(v). The lower tail Q(x) = Phi(-x) = e^(-x^2 / 2) R(x) for x = |v|, where R falls smoothly

@@ -17,12 +17,14 @@
 // linear_split_kernel (few tokens): bound by the bytes of W. One pair per tile and K slice; the
 // slices of a tile are a cluster, which adds its fp32 partial sums through distributed shared
 // memory in slice order. One launch, no workspace, and the same sum in every run. (128 x 7168 x
-// 16384 bf16: 45 us against 36 for W's bytes; 8 bits: 27 against 18. One token, 16384 x 7168: 37.6
-// and 21.4.)
+// 16384 bf16 with a residual: 45 us in a short run, 49 in a long one, against 36 for W's bytes; 8
+// bits: 31 against 18.)
 //
 // linear_pair_kernel (many tokens): bound by the tensor cores. Persistent pairs, with two
 // accumulators in TMEM so that a tile's epilogue runs under the next tile's main loop (16384 x
-// 8192 x 7168 bf16: 1.24 ms, 1.56 PFLOP/s, in a short run; 1.45 ms under the power cap).
+// 8192 x 7168 bf16: 1.24 ms, 1.56 PFLOP/s, in a short run; 1.45 ms under the power cap). It also
+// serves few tokens where there are feature tiles for most pairs and one wave of them streams W
+// as fast as slices would (one token, 16384 x 7168: 38 us, 8 bits 21, against 36 and 18).
 #pragma once
 
 #include "common.cuh"

@@ -1534,8 +1534,11 @@ mla_status launch_linear_pair(const void* x, const void* W, mla::lin::Params p, 
 // Which kernel, tokens per tile and K slices. Both kernels' times are estimated from the sizes
 // and the cheapest of a few candidates taken. The constants (microseconds, bytes per
 // microsecond) were fitted to 340 sizes on a B200, T = 1 .. 4096, N = 130 .. 16384, K = 300 ..
-// 16384, both operand types, 3,000 measured variants: the pick is within 1.6 % of the fastest
-// variant on the (geometric) average and 30 % off at worst. What decides, per K block of a CTA:
+// 16384, both operand types, 3,000 measured variants: the pick was within 1.6 % of the fastest
+// variant on the (geometric) average and 30 % off at worst. That was with bare outputs and an
+// epilogue of eight warps in the many-token kernel for every N, the narrow form of now; the wide
+// form is faster, an activation slower, and the estimate knows of neither (16384 x 1024 x 512: 224
+// tokens a tile 6 to 9 % faster than the pick). What decides, per K block of a CTA:
 // its 16 KiB of W and 64 bytes a token of x through the SM's 100-107 KB/us, or the MMA's 0.82
 // ns a token; over all CTAs: the operands' bytes from HBM; and behind that the epilogue.
 struct LinearChoice {
@@ -1575,7 +1578,8 @@ LinearChoice choose_linear(const mla::lin::Params& p, bool f8, int sms, int max_
       const double tiles = tiles_n * std::ceil((double)p.T / nt);
       for (int slices = 1; slices <= max_slices; slices *= 2) {
         if (slices > 1 && 2 * slices > kblk) break;
-        // clusters of 2 * slices CTAs that fit at once, at one CTA an SM: GPCs hold 16 to 20 SMs
+        // clusters of 2 * slices CTAs that fit at once, at one CTA an SM: a B200's GPCs hold 16 to 20
+        // SMs (an estimate of waves only; how many slices can run at all is max_slices)
         const int fit = slices == 1 ? (int)pairs : slices == 2 ? 36 : slices == 4 ? 14 : 7;
         const bool two = two_an_sm(nt, slices, tiles, sms);
         if (slices == kMaxSlices && tiles > fit) break;

@@ -162,7 +162,8 @@ class LayerStep:
     [H*Dv, M] (each out x in). projections="fp8": the query, gate and output projections
     run in 8 bits, their weights quantised here once (finished on return, so that any stream
     may run the step); the cache write keeps bf16 rows. The step's tensors and its cache must be
-    bf16. One run of an object at a time: its buffers are the step's.
+    bf16, its geometry the cache write's (R = 512, Dr = 64, pages of 64, M a multiple of 64).
+    One run of an object at a time: its buffers are the step's.
 
     A first layer, or one whose input already is the residual stream (another layer's y), runs
     with residual=None: the stream is then x itself, which is read until the run's end."""

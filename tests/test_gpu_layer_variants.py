@@ -191,3 +191,19 @@ def test_layer_step_adds_its_output_projection(projections, H, M, lens):
     err = np.abs(host(lay.y) - ref)
     assert np.all(err <= bound), f"worst {np.max(err / bound):.3f} of the bound"
     assert np.mean(np.abs(orc.round_bf16(r) - ref) > bound) > 0.5
+
+
+# ----------------------------------------------------------------------------- activations of very negative sums
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+def test_activations_vanish_where_their_exponential_does(act):
+    """From 1 + e^-v = 2^126 on, v = -87.3, the quotient may be 0: sigmoid is below 1.2e-38 there and
+    silu below 1.1e-36; above it both are within the store's half step and 2^-18."""
+    v = wl.bf16_bits_to_f32(np.arange(0xC2A0, 0xC2DD, dtype=np.uint16)).astype(np.float64)      # -80 .. -110
+    assert v[0] == -80 and v[-1] == -110
+    x, W = np.zeros((len(v), 16)), np.zeros((8, 16))
+    x[:, 2], W[:, 2] = v, 1
+    out = torch.empty(len(v), 8, dtype=torch.bfloat16, device=DEV)
+    code = {"sigmoid": mla.MLA_ACT_SIGMOID, "silu": mla.MLA_ACT_SILU}[act]
+    mla.mla_linear(bf16(x), bf16(W), None, None, None, out, len(v), 8, 16, code)
+    ref = layer.activation(v, act)[:, None]
+    assert np.all(np.abs(host(out) - ref) <= (2.0 ** -8 + 2.0 ** -18) * np.abs(ref) + {"sigmoid": 1.2e-38, "silu": 1.1e-36}[act])
