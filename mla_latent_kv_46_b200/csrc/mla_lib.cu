@@ -1705,6 +1705,8 @@ mla_status mla_debug_linear_choice(int32_t T, int32_t N, int32_t K, int32_t eigh
     if (mla_status s = eight_bit ? most_slices<true>(&slices) : most_slices<false>(&slices)) return s;
     max_slices = slices;
   }
+  if (max_slices < 1 || max_slices > mla::lin::kMaxSlices)
+    return fail(MLA_ERR_INVALID, "debug_linear_choice: max_slices=%d", max_slices);
   mla::lin::Params p{};
   const __nv_bfloat16 given{};      // (the choice looks at which operands there are, not at them)
   p.mul = operands > 0 ? &given : nullptr;

@@ -33,7 +33,8 @@ def test_choices_are_launchable(sms):
 
 @pytest.mark.parametrize("bad", [(0, 8, 16), (1, 0, 16), (1, 8, 0), (1, 8, 2 ** 31 - 1)])
 def test_bad_arguments_are_refused(bad):
-    for args in ((*bad, 0, 0), (1, 8, 16, 0, 3), (1, 8, 16, 0, -1)):
+    for args in ((*bad, 0, 0, SMS, 8), (1, 8, 16, 0, 3, SMS, 8), (1, 8, 16, 0, -1, SMS, 8), (1, 8, 16, 0, 0, SMS, 0),
+                 (1, 8, 16, 0, 0, SMS, 16)):
         with pytest.raises(mla.MlaError) as e:
-            mla.mla_debug_linear_choice(*args, SMS, 8)
+            mla.mla_debug_linear_choice(*args)
         assert e.value.status == mla._binding.MLA_ERR_INVALID
