@@ -316,12 +316,12 @@ add_rmsnorm_kernel(const Params p) {
 // shared memory that bulk copies keep full while the block works on the oldest row. ITEMS
 // granules a thread, whose gains it keeps for every row. One barrier per row: once it has
 // passed, every thread holds its part of the row in registers and the buffer is loaded
-// again. It is not instantiated for the quantiser, which has a block a row (16384 x 8192
-// bf16: 114 us, 61 for the bytes). The inputs are read
-// once, so they are loaded with evict-first priority, which
+// again. The inputs are read once, so they are loaded with evict-first priority, which
 // leaves L2 to the writes (T = 16384, M = 7168, bf16 with a residual: 155 us, 6.05 TB/s,
 // against 169 us without, and 204 for the kernel above; two buffers and four granules a
 // thread beat three buffers, or two or eight granules). Shifted rows gained nothing here.
+// It is not instantiated for the quantiser, which has a block a row (16384 x 8192 bf16: 114 us,
+// 61 for the bytes).
 constexpr int kStages = 2;
 constexpr int kStreamThreads = 512;
 
